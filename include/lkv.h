@@ -370,6 +370,214 @@ LKV_API int lkv_tiered_decode(int B, int Hq, int Hkv, int T_cap, int D, int grou
                       float *out, int64_t *skip_counts, void *workspace, size_t ws_bytes,
                       void *stream);
 
+/* ------------------------------------------------------------------------
+ * One serving step around the decode: page plan, rotary tables, norm +
+ * rotation + append, and attention of one or a few new tokens.  A step is
+ *   lkv_page_plan            lengths, pages and slots of the new tokens
+ *   lkv_rope_append_kv       their queries, and their K and V in the cache
+ *   lkv_decode_attention_multi[_paged]
+ * on one stream, with lkv_rope_table once beforehand.  Nothing in a step is
+ * read by the host, so it can be captured into a CUDA graph.  int32 and f32
+ * vectors of these calls (lengths, offsets, slopes, ...) need 4-byte
+ * alignment only, int64 ones 8; tensors need 16.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * lkv_page_plan -- block tables, lengths and slot maps of a ragged batch,
+ * built on the device ([TQ] §与其他优化技术的对比: the cache is meant to work
+ * with paged KV management).  Sequence b holds L_b = seq_lens[b] cached
+ * tokens and brings N_b = n_new[b] >= 0 more.  It is valid when L_b >= 0,
+ * N_b >= 0 and L_b + N_b <= pages_per_seq * LKV_PAGE_TOKENS.  With
+ * P(x) = ceil(x / LKV_PAGE_TOKENS) it needs P(L_b + N_b) - P(L_b) pages.
+ * Sequences are served in order up to the first whose tokens pass n_cap or
+ * whose pages pass *free_count (running sums over the valid ones); that one
+ * and all behind it, and invalid ones, keep their length and get nothing.
+ * Pages come off the end of the stack: the k-th page taken (in order of
+ * sequence, then position) is free_pages[*free_count - 1 - k].
+ *
+ *   seq_lens, n_new  in   int32 [B]
+ *   free_pages   in   int32 [free_cap]; free_count  in  int32 [1], clamped
+ *                     into [0, free_cap]
+ *   block_table  in/out  int32 [B][pages_per_seq]: entries of the new pages
+ *                     are written, the others kept
+ *   new_lens     out  int32 [B]  L_b plus the tokens served
+ *   cu_new       out  int32 [B + 1]  running sum of the tokens served: the
+ *                     rows of sequence b are [cu_new[b], cu_new[b + 1])
+ *   positions    out  int32 [n_cap]  position of each new token
+ *   token_seq    out  int32 [n_cap]  its sequence
+ *   slots        out  int64 [n_cap]  page * LKV_PAGE_TOKENS + offset; -1 when
+ *                     the page id lies outside [0, num_pages)
+ *                     (all three: rows from cu_new[B] on are left as they were)
+ *   free_left    out  int32 [1]  pages still on the stack
+ *   status       out  nullable int32 [1]: LKV_OK, or LKV_ERR_INVALID_ARG when
+ *                     some sequence was invalid or not served, or a page id
+ *                     was out of range
+ *
+ * At most 16384 sequences (LKV_ERR_UNSUPPORTED).  No output may overlap an
+ * input or another output (LKV_ERR_INVALID_ARG): every block reads all the
+ * lengths, so new_lens must be another buffer than seq_lens.
+ */
+LKV_API int lkv_page_plan(int B, int pages_per_seq, int num_pages, int n_cap, const int32_t *seq_lens,
+                  const int32_t *n_new, const int32_t *free_pages, int free_cap,
+                  const int32_t *free_count, int32_t *block_table, int32_t *new_lens,
+                  int32_t *cu_new, int32_t *positions, int32_t *token_seq, int64_t *slots,
+                  int32_t *free_left, int32_t *status, void *stream);
+
+/* How the frequencies of the rotary positions are scaled for long contexts. */
+enum lkv_rope_kind {
+    LKV_ROPE_NONE = 0,   /* f_i = inv_i = base^(-2 i / rot_dim) */
+    LKV_ROPE_LINEAR = 1, /* f_i = inv_i / factor */
+    LKV_ROPE_SMOOTH = 2, /* by turns within the original context: with
+                            w = clamp((orig_ctx inv_i / 2 pi - low) / (high - low), 0, 1),
+                            f_i = (1 - w) inv_i / factor + w inv_i */
+    LKV_ROPE_RAMP = 3    /* by dimension: with d(n) = rot_dim ln(orig_ctx / (2 pi n)) / (2 ln base),
+                            a = max(floor(d(high)), 0), z = min(ceil(d(low)), rot_dim - 1) and
+                            w = clamp((i - a) / max(z - a, 0.001), 0, 1),
+                            f_i = w inv_i / factor + (1 - w) inv_i */
+};
+
+typedef struct {
+    int32_t kind;       /* an lkv_rope_kind */
+    int32_t rot_dim;    /* channels that turn: a multiple of 16, 16 to 128 */
+    double base;        /* > 1 */
+    double factor;      /* > 0 (kinds 1 to 3) */
+    double low, high;   /* 0 < low < high (kinds 2 and 3) */
+    double orig_ctx;    /* > 0 (kinds 2 and 3) */
+    double attn_factor; /* multiplies every value; 1 for none */
+} lkv_rope_spec;
+
+/*
+ * lkv_rope_table -- table[p][i] = attn_factor * (cos, sin)(p f_i) for
+ * positions p < rows and pairs i < rot_dim / 2, from fp64 angles, each value
+ * rounded once to f32.  Made once per model.
+ *
+ *   table  out  f32 [rows][rot_dim / 2][2]
+ */
+LKV_API int lkv_rope_table(lkv_rope_spec spec, int rows, float *table, void *stream);
+
+/*
+ * lkv_rope_append_kv -- the new tokens of a ragged batch on their way into
+ * attention, in one pass: RMS norm of every query and key head, rotary
+ * positions, and the quantized append of lkv_append_kv at any number of slots.  Every
+ * fp32 operation is rounded on its own (no fused multiply-add).  For a query
+ * or key head x of D channels of token t:
+ *   norm (when its weight is given): ss = sum x_i^2 summed pairwise, adjacent
+ *     values first; y_i = (x_i * (1 / sqrt(ss * (1 / D) + eps))) * weight_i
+ *   rotation: with (c, s) = table[positions[t]][i], the pair (a, b) becomes
+ *     (a c - b s, b c + a s); pair i is channels (i, i + rot_dim / 2), or
+ *     (2 i, 2 i + 1) when interleaved; channels from rot_dim on stay
+ *   one rounding to bf16.
+ * Keys then, and values as they come, are quantized as lkv_quantize_kv does
+ * and written at slots[t]: row slots[t] % page_tokens of page slots[t] /
+ * page_tokens of [num_pages][Hkv][page_tokens] rows.  A paged cache has
+ * page_tokens = LKV_PAGE_TOKENS; the contiguous cache [B][Hkv][T_cap] is
+ * num_pages = B, page_tokens = T_cap, slot b * T_cap + t.
+ *
+ *   n_tokens   in  nullable int32 [1]: tokens there are (clamped into
+ *                  [0, n_cap]; NULL: n_cap).  Rows behind them are not read,
+ *                  and nothing is written for them
+ *   positions  in  int32 [n_cap] (may be NULL when rot_dim == 0); a token
+ *                  whose position lies outside [0, table_rows) is left out:
+ *                  nothing is written for it
+ *   slots      in  int64 [n_cap]; outside [0, num_pages * page_tokens): the
+ *                  token's K and V are not written.  Slots of one call must
+ *                  differ: what equal ones leave behind is unspecified
+ *   q, k, v    in  bf16, token t at q + t * q_stride elements (a multiple of
+ *                  8, at least heads * D), its heads [H][D] side by side: the
+ *                  parts of one fused projection, or tensors of their own
+ *   q_weight, k_weight  in  bf16 [D], nullable (no norm)
+ *   table      in  f32 [table_rows][rot_dim / 2][2] (unused for rot_dim 0)
+ *   q_out      out bf16 [n_cap][Hq][D]; must not overlap q, k or v
+ *   k_codes, k_sz, v_codes, v_sz  in/out  the packed cache
+ *
+ *   reciprocal  0: the quantizer of lkv_quantize_kv, bit for bit.  1: its two
+ *                  divisions become products with a reciprocal, scale =
+ *                  d * (1 / qmax) and inv = (1 / d) * qmax, each operation
+ *                  rounded -- what tensor libraries compute for a division by,
+ *                  or of, a constant.  Codes and pairs are then bit for bit
+ *                  those of a cache quantized with plain tensor operations
+ *                  (the two differ in the last place of a pair, and in a code
+ *                  where a value lies between two codes)
+ *
+ * rot_dim is a multiple of 16 up to D (LKV_ERR_UNSUPPORTED).
+ */
+LKV_API int lkv_rope_append_kv(lkv_qspec spec, int n_cap, int Hq, int Hkv, int num_pages,
+                  int page_tokens, int D, const int32_t *n_tokens, const int32_t *positions,
+                  const int64_t *slots, const void *q, int64_t q_stride, const void *k,
+                  int64_t k_stride, const void *v, int64_t v_stride, const void *q_weight,
+                  const void *k_weight, float eps, int rot_dim, int interleaved,
+                  const float *table, int table_rows, void *q_out, void *k_codes, float *k_sz,
+                  void *v_codes, float *v_sz, int reciprocal, void *stream);
+
+/* Scores and visibility of lkv_decode_attention_multi. */
+typedef struct {
+    float softmax_scale;        /* finite */
+    float softcap;              /* c > 0: scores become c * tanh(score / c); 0: none */
+    int32_t window;             /* w > 0: a query sees the last w positions, its own among them; 0: all */
+    const float *slopes;        /* device f32 [Hq], nullable: slopes[h] * (t - p) is added to the score */
+    const int32_t *prefix_lens; /* device int32 [B], nullable: positions before it are visible to every query */
+    const int32_t *doc_starts;  /* device int32 [B], nullable: first position of the queries' document */
+} lkv_score_rule;
+
+/*
+ * lkv_decode_attention_multi -- attention of the newest tokens of every
+ * sequence (one, or a short run such as drafted tokens under verification)
+ * over the packed cache that already holds them.  T = seq_lens[b]; the n
+ * query rows of sequence b are rows cu_q[b] .. cu_q[b + 1] of q (without
+ * cu_q: row b alone), and the i-th stands at position p = T - n + i.  It sees
+ * position t < T when t < prefix_lens[b], or when doc_starts[b] <= t <= p and
+ * p - t < window.  For head h of KV head g = h / r:
+ *   x_t = softmax_scale * sum_d q[d] khat_t[d], capped, then biased (see
+ *         lkv_score_rule)
+ *   out = sum_t exp(x_t) vhat_t / sum_t exp(x_t) over the visible t
+ *   lse = ln sum_t exp(x_t)
+ * A query that sees nothing gets out = 0 and lse = -infinity.  Arithmetic
+ * keeps fp32 accuracy, and results do not depend on timing.  (scale, zero)
+ * and 16-bit values at positions that no query of the sequence sees may be
+ * anything, infinities and NaN among them.
+ *
+ *   max_q      most query rows of one sequence, 1 to 64: rows past it are not
+ *              computed
+ *   n_rows     rows of q, out and lse
+ *   seq_lens   in   int32 [B]
+ *   cu_q       in   nullable int32 [B + 1], rising, within [0, n_rows]; rows
+ *                   outside every sequence are left as they were
+ *   q          in   bf16 [n_rows][Hq][D]
+ *   k_codes... in   the packed cache (any pair of widths, any group of up to
+ *                   64 query heads)
+ *   out        out  f32 [n_rows][Hq][D]
+ *   lse        out  nullable f32 [n_rows][Hq]
+ *   workspace  in/out  lkv_multi_workspace_bytes() bytes, 256-byte aligned,
+ *              zero-filled before its first use; every call leaves it ready
+ *              for the next one, of any sizes that it is large enough for.
+ *              Calls that overlap on the GPU, captured graphs among them,
+ *              must not share one, and it is not a workspace of the other
+ *              decode calls.  Bytes
+ *              [0, 16) as in lkv_decode_workspace_bytes: the status word is
+ *              LKV_ERR_INVALID_ARG after a length outside [0, T_cap], row
+ *              offsets out of order or range, more than max_q rows, or a page
+ *              id out of range (page 0 is read instead).
+ *
+ * At most 8192 sequences, T_cap up to 2^30, and 2^31 tiles of 16 or 32 tokens over all
+ * sequences, heads and blocks of query rows (LKV_ERR_UNSUPPORTED).
+ */
+LKV_API size_t lkv_multi_workspace_bytes(lkv_qspec spec, int B, int Hq, int Hkv, int T_cap, int D,
+                         int max_q);
+
+LKV_API int lkv_decode_attention_multi(lkv_qspec spec, int B, int Hq, int Hkv, int T_cap, int D,
+                         int max_q, int n_rows, const int32_t *seq_lens, const int32_t *cu_q,
+                         const void *q, const void *k_codes, const float *k_sz,
+                         const void *v_codes, const float *v_sz, lkv_score_rule rule, float *out,
+                         float *lse, void *workspace, size_t ws_bytes, void *stream);
+
+/* The same over a paged cache, T_cap = pages_per_seq * LKV_PAGE_TOKENS. */
+LKV_API int lkv_decode_attention_multi_paged(lkv_qspec spec, int B, int Hq, int Hkv,
+                         int pages_per_seq, int num_pages, int D, int max_q, int n_rows,
+                         const int32_t *seq_lens, const int32_t *cu_q, const void *q,
+                         const int32_t *block_table, const void *k_pool, const float *k_sz_pool,
+                         const void *v_pool, const float *v_sz_pool, lkv_score_rule rule,
+                         float *out, float *lse, void *workspace, size_t ws_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -25,7 +25,7 @@ NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "--expt-relaxed-constexpr", "-Xc
 # (scale, zero), tiers and positions): no multiply-add contraction, so a
 # plain a * b + c there can never turn into one fused operation.  The
 # decode's deliberate fused operations live in other files.
-NO_FMAD = ("quantize.cu", "tier.cu")
+NO_FMAD = ("quantize.cu", "tier.cu", "rope_append.cu")
 
 
 def extra_flags(src):

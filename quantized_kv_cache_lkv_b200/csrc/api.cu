@@ -5,9 +5,9 @@
 #include <cstdint>
 #include <cstring>
 
-#include "../../include/lkv.h"
 #include <algorithm>
 
+#include "api_common.cuh"
 #include "fused_impl.cuh"
 #include "lkv_kernels.cuh"
 
@@ -28,20 +28,6 @@ int num_sms() {
 namespace {
 
 constexpr int kChunk = 256;       // decode rows per chunk
-constexpr size_t kAlign = 256;
-constexpr size_t kHeaderBytes = 256;  // status, wait limit, done counter, skip-count accumulators
-
-size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
-
-// 16 is the passthrough width: the row holds the bf16 values, with no (scale, zero)
-bool bits_ok(int b) { return b == 2 || b == 4 || b == 6 || b == 8 || b == 16; }
-bool dim_ok(int D) { return D == 64 || D == 128; }
-bool group_ok(int G, int D) { return (G == 32 || G == 64 || G == 128) && G <= D && D % G == 0; }
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-// A pointer that must be valid when its tensor is non-empty.
-bool ptr_ok(const void* p, bool nonempty) { return !nonempty || (p != nullptr && aligned16(p)); }
-
-int from_cuda(cudaError_t e) { return e == cudaSuccess ? LKV_OK : LKV_ERR_CUDA; }
 
 struct WsLayout {
   size_t status, logits, stats, partial, total;
@@ -201,13 +187,6 @@ int check_attention_shape(int B, int Hq, int Hkv, int T_cap, int D, int G) {
   if (!dim_ok(D) || !group_ok(G, D)) return LKV_ERR_UNSUPPORTED;
   const int r = Hq / Hkv;
   if (r > 64 || !(r == 1 || r == 2 || r % 4 == 0)) return LKV_ERR_UNSUPPORTED;
-  if (((long long)T_cap * (D / G)) % 2 != 0) return LKV_ERR_UNSUPPORTED;
-  return LKV_OK;
-}
-
-int check_cache_shape(int B, int Hkv, int T_cap, int D, int G) {
-  if (B < 0 || Hkv <= 0 || T_cap < 0) return LKV_ERR_INVALID_ARG;
-  if (!dim_ok(D) || !group_ok(G, D)) return LKV_ERR_UNSUPPORTED;
   if (((long long)T_cap * (D / G)) % 2 != 0) return LKV_ERR_UNSUPPORTED;
   return LKV_OK;
 }

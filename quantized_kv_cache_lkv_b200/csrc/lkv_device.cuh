@@ -230,9 +230,11 @@ __device__ __forceinline__ uint32_t wide_quant_code(const WideQuant& q, float x,
 // `one` must be 1.0f, passed in at run time (see the rounding step).
 // Otherwise (inv overflowing for a tiny d, or d overflowing) every value takes
 // the scalar path of wide_quant_code.  `mask` names the lanes of the calling row.
+// With `reciprocal`, scale = d * (1 / qmax) and inv = (1 / d) * qmax, each
+// operation rounded: at most 2 and 1 units in the last place away.
 template <int BITS>
 __device__ __forceinline__ void quantize16(const uint32_t (&w)[8], int lpg, unsigned mask, float one,
-                                           LaneWords<BITS>& lw, float& scale, float& zero) {
+                                           LaneWords<BITS>& lw, float& scale, float& zero, bool reciprocal = false) {
   // min and max are exact in bf16, two values per instruction
   __nv_bfloat162 lo = *reinterpret_cast<const __nv_bfloat162*>(&w[0]), hi = lo;
 #pragma unroll
@@ -256,8 +258,13 @@ __device__ __forceinline__ void quantize16(const uint32_t (&w)[8], int lpg, unsi
   float inv = 0.0f;
   scale = 0.0f;
   if (d != 0.0f) {
-    scale = __fdiv_rn(d, qmax);
-    inv = __fdiv_rn(qmax, d);
+    if (reciprocal) {
+      scale = __fmul_rn(d, __fdiv_rn(1.0f, qmax));
+      inv = __fmul_rn(__fdiv_rn(1.0f, d), qmax);
+    } else {
+      scale = __fdiv_rn(d, qmax);
+      inv = __fdiv_rn(qmax, d);
+    }
   }
   zero = __fadd_rn(mn, 0.0f);
   if (d <= 3.4028234663852886e38f && inv <= 3.4028234663852886e38f) {

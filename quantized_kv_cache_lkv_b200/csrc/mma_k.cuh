@@ -108,15 +108,14 @@ __device__ __forceinline__ uint32_t hsub2_u32(uint32_t a, uint32_t b) {
 }
 
 // Register J (0 .. D/8 - 1) of a lane slice held in words w (the slice's
-// D*KB/128 words): two codes as exact fp16 values c * 2^off.
+// D*KB/128 words): two codes under the fp16 pattern, 1024 + c * 2^off.
 template <int KB, int J, int SW>
-__device__ __forceinline__ uint32_t a_reg_codes(const uint32_t (&w)[SW]) {
+__device__ __forceinline__ uint32_t a_reg_bits(const uint32_t (&w)[SW]) {
   constexpr PlanEntry pe = Plan<KB>::e[J % 8];
   constexpr int p = pe.p + (J / 8) * 16 * KB;  // first bit of the window in the slice
   constexpr int wi = p / 32, sh = p % 32;
-  uint32_t r;
   if constexpr (KB == 8) {
-    r = __byte_perm(w[wi], 0x64646464u, (J & 1) ? 0x4341 : 0x4240);
+    return __byte_perm(w[wi], 0x64646464u, (J & 1) ? 0x4341 : 0x4240);
   } else {
     // highest bit of the window that holds code bits
     constexpr int top = sh + 16 + pe.hi_off + KB - 1;
@@ -130,9 +129,14 @@ __device__ __forceinline__ uint32_t a_reg_codes(const uint32_t (&w)[SW]) {
     }
     constexpr uint32_t m = (1u << KB) - 1u;
     constexpr uint32_t mask = (m << pe.lo_off) | (m << (16 + pe.hi_off));
-    r = (win & mask) | kF16Magic2;
+    return (win & mask) | kF16Magic2;
   }
-  return hsub2_u32(r, kF16Magic2);
+}
+
+// The same as exact fp16 values c * 2^off.
+template <int KB, int J, int SW>
+__device__ __forceinline__ uint32_t a_reg_codes(const uint32_t (&w)[SW]) {
+  return hsub2_u32(a_reg_bits<KB, J, SW>(w), kF16Magic2);
 }
 
 // At the 16-bit passthrough width the slice holds bf16 values: register J

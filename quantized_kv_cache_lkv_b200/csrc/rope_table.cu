@@ -1,0 +1,90 @@
+// rope_table.cu -- cos and sin tables of the rotary positions
+// (lkv_rope_table).
+//
+// Row p, pair i: attn * (cos, sin)(p f_i).  An angle p f_i of a far position
+// has few bits of fraction left in fp32, so the angles are taken in fp64, and
+// to keep the fp64 work small each block evaluates sincos only at its first
+// row, at one slab of rows and at one row, and reaches the others by the
+// addition theorem:
+//   (cos, sin)(x + y) = (cos x cos y - sin x sin y, sin x cos y + cos x sin y),
+// four fp64 operations a value pair, at most 32 steps from an evaluated angle
+// (error below 1e-14, rounded once to fp32).  Bound by the table's write.
+#include <algorithm>
+#include <cmath>
+
+#include "serving.cuh"
+
+namespace lkv {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kRun = 32;      // rows of one thread
+constexpr int kMaxHalf = 64;  // rot_dim <= 128
+
+// The frequency of pair i.
+__device__ double frequency(const RopeTableArgs& a, int i) {
+  const double f = exp2(-log2(a.base) * (double)i / (double)a.half);
+  const double two_pi = 6.283185307179586476925286766559;
+  if (a.kind == 1) return f / a.factor;
+  if (a.kind == 2) {  // by turns inside the original context
+    const double g = (a.orig * f / two_pi - a.low) / (a.high - a.low);
+    const double mix = fmin(fmax(g, 0.0), 1.0);
+    return (1.0 - mix) * (f / a.factor) + mix * f;
+  }
+  if (a.kind == 3) {  // by dimension
+    const double rot = 2.0 * a.half;
+    const double lo = fmax(floor(rot * log(a.orig / (a.high * two_pi)) / (2.0 * log(a.base))), 0.0);
+    const double hi = fmin(ceil(rot * log(a.orig / (a.low * two_pi)) / (2.0 * log(a.base))), rot - 1.0);
+    const double mix = fmin(fmax(((double)i - lo) / fmax(hi - lo, 0.001), 0.0), 1.0);
+    return f / a.factor * mix + f * (1.0 - mix);
+  }
+  return f;
+}
+
+__device__ __forceinline__ double2 turn(double2 x, double2 y) {
+  return make_double2(x.x * y.x - x.y * y.y, x.y * y.x + x.x * y.y);
+}
+
+__global__ void __launch_bounds__(kThreads) rope_table_kernel(RopeTableArgs a, int slabs) {
+  __shared__ double2 s_base[kMaxHalf], s_slab[kMaxHalf], s_one[kMaxHalf];
+  const int tid = threadIdx.x;
+  const long long p0 = (long long)blockIdx.x * slabs * kRun;
+  // one evaluation a thread: three angles of each pair
+  if (tid < 3 * a.half) {
+    const int i = tid % a.half, which = tid / a.half;
+    const double f = frequency(a, i);
+    double2 v;
+    sincos(f * (which == 0 ? (double)p0 : which == 1 ? (double)kRun : 1.0), &v.y, &v.x);
+    if (which == 0) s_base[i] = make_double2(v.x * a.attn, v.y * a.attn);
+    else if (which == 1) s_slab[i] = v;
+    else s_one[i] = v;
+  }
+  __syncthreads();
+  const int i = tid % a.half, slab = tid / a.half;
+  if (slab >= slabs) return;
+  double2 v = s_base[i];
+  const double2 by = s_slab[i], one = s_one[i];
+  for (int k = 0; k < slab; ++k) v = turn(v, by);
+  long long p = p0 + (long long)slab * kRun;
+  const long long end = p + kRun < a.rows ? p + kRun : a.rows;
+  float2* dst = reinterpret_cast<float2*>(a.table) + p * a.half + i;
+#pragma unroll 4
+  for (; p < end; ++p, dst += a.half) {
+    *dst = make_float2((float)v.x, (float)v.y);
+    v = turn(v, one);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_rope_table(const RopeTableArgs& a, cudaStream_t s) {
+  if (a.rows == 0) return cudaSuccess;
+  const int slabs = std::max(1, std::min(kThreads / a.half, 8));
+  const long long rows = (long long)slabs * kRun;
+  const long long blocks = (a.rows + rows - 1) / rows;
+  rope_table_kernel<<<(unsigned)blocks, kThreads, 0, s>>>(a, slabs);
+  return cudaGetLastError();
+}
+
+}  // namespace lkv
