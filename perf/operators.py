@@ -465,7 +465,8 @@ def _append_own(s, lkv, kept):
     wq, wk = (s["weights"][0], s["weights"][1]) if c["norm"] else (None, None)
     lkv.lkv_rope_append_kv((c["kb"], c["vb"], c["G"]), s["pos"].numel(), c["Hq"], c["Hkv"], s["pages"], s["page_tokens"], c["D"],
                            s["count"], s["pos"], s["slots"], s["q"], s["k"], s["v"], wq, wk, s["eps"], c["rot"], c["inter"],
-                           s["table"], s["table"].shape[0], s["q_out"], s["k_codes"], s["k_sz"], s["v_codes"], s["v_sz"])
+                           s["table"], s["table"].shape[0], s["q_out"], s["k_codes"], s["k_sz"], s["v_codes"], s["v_sz"],
+                           reciprocal=True)  # what a tensor program's divisions by constants compute
     return {k: s[k] for k in ("q_out", "k_codes", "k_sz", "v_codes", "v_sz")}
 
 
