@@ -558,7 +558,7 @@ typedef struct {
  *              offsets out of order or range, more than max_q rows, or a page
  *              id out of range (page 0 is read instead).
  *
- * At most 8192 sequences, T_cap up to 2^30, and 2^31 tiles of 16 or 32 tokens over all
+ * At most 4096 sequences, T_cap up to 2^30, and 2^31 tiles of 16 or 32 tokens over all
  * sequences, heads and blocks of query rows (LKV_ERR_UNSUPPORTED).
  */
 LKV_API size_t lkv_multi_workspace_bytes(lkv_qspec spec, int B, int Hq, int Hkv, int T_cap, int D,

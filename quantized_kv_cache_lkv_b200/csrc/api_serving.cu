@@ -29,9 +29,9 @@ int multi_shape(lkv_qspec spec, int B, int Hq, int Hkv, int T_cap, int D, int ma
   multi::MultiArgs& a = c.a;
   a.B = B; a.Hq = Hq; a.Hkv = Hkv; a.T_cap = T_cap; a.G = spec.group; a.r = Hq / Hkv; a.max_q = max_q;
   a.kb = spec.k_bits; a.vb = spec.v_bits;
-  if (!multi::plan_multi(a, D, c.p)) return LKV_ERR_UNSUPPORTED;
+  multi::plan_multi(a, D, c.p);
   // tiles are numbered in 32 bits
-  if ((double)B * a.units_max * ((double)T_cap / a.tt + 2.0) >= 2147483647.0) return LKV_ERR_UNSUPPORTED;
+  if ((double)B * c.p.units_max * ((double)T_cap / c.p.sh.tt + 2.0) >= 2147483647.0) return LKV_ERR_UNSUPPORTED;
   return LKV_OK;
 }
 
@@ -72,7 +72,14 @@ int multi_impl(lkv_qspec spec, int B, int Hq, int Hkv, int T_cap, int D, int max
   a.arrive = reinterpret_cast<int*>(ws + c.p.ws_arrive);
   a.pieces = reinterpret_cast<float*>(ws + c.p.ws_pieces);
   a.cpieces = reinterpret_cast<float*>(ws + c.p.ws_cpieces);
-  return from_cuda(multi::launch_multi(a, D, c.p, static_cast<cudaStream_t>(stream)));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  switch (a.kb) {
+    case 2: return from_cuda(multi::launch_multi_k2(a, D, c.p, s));
+    case 4: return from_cuda(multi::launch_multi_k4(a, D, c.p, s));
+    case 6: return from_cuda(multi::launch_multi_k6(a, D, c.p, s));
+    case 8: return from_cuda(multi::launch_multi_k8(a, D, c.p, s));
+    default: return from_cuda(multi::launch_multi_k16(a, D, c.p, s));
+  }
 }
 
 }  // namespace

@@ -8,37 +8,42 @@
 // over the visible t.  With khat = scale * code + zero per group of channels,
 //   q . khat_t = sum_g scale_tg (q_g . code_tg) + zero_tg (sum of q_g)
 //   out        = sum_t (e_t scale_tg) code_tg + sum_t e_t zero_tg
-// so both products run on integer codes, exact in 16-bit floating point.  They
-// are centred, code - 2^(bits-1) with zero + 2^(bits-1) scale: with codes from 0 up
-// the two terms are large and cancel (8-bit K: rel-L2 1.2e-5 instead of 1e-6).
+// so both products run on integer codes, exact in fp16.  The codes are
+// centred -- any integer may move from the codes into zero -- because with
+// codes from 0 up the two terms are large and cancel.  V takes the middle code.
+// K takes the code nearest to the value 0: its outlier channels stretch the
+// range of a group, and the middle can lie far from most of its values.
 //
 // What bounds it: the packed rows, read once (K6V4, D 128, G 64: 192 bytes a
-// row, 8.3 clocks of one SM at the copy bandwidth), and close behind the
-// instructions that turn codes into MMA operands.  So:
+// row, 8.3 clocks of one SM at the copy bandwidth), and the instructions that
+// turn codes into MMA operands, which take longer than the bytes.  So:
 //   - tokens are the M rows of mma.m16n8k16 in the K product and its K rows in
 //     the V product, and the query rows (heads of the group x new tokens) its
 //     N = 8 columns: with 1 to 8 query rows nothing but columns is padded;
-//   - K codes become fp16 integers (mma_k.cuh) against q scaled by a power of
-//     two: exact products.  V codes become bf16 integers against e * scale
-//     split in two bf16 terms (hi + lo leaves at most 2^-18 of the product);
+//   - K codes become fp16 integers against q scaled by a power of two
+//     (mma_k.cuh): exact products.  V codes become fp16 integers against
+//     e * scale split in two fp16 terms (22 bits), the scales taken relative
+//     to a power of two above them so that e * scale stays below 2^15.  At the
+//     16-bit width both products are bf16, e split in three terms;
 //   - the channel-to-row and token-to-slot orders of the MMAs are free, so
 //     every lane reads whole runs of codes of one token from shared memory,
 //     and the codes of two tokens are paired by one byte permute per half
 //     word, before they are unpacked;
-//   - the running maximum moves only when it would grow by more than 2^8
-//     (e stays far inside fp32), so rescaling is rare.
+//   - what depends on a token alone -- centring, the check of the scales, the
+//     zeroing of what nobody sees -- is done once, by the lane of that token,
+//     in the tile's (scale, zero) rows in shared memory;
+//   - the reference exponent is an integer and moves only when a score passes
+//     it by 2^8, so rescaling is rare and exact.
 //
-// Work split: the tiles (kTile tokens or half of it) of all units -- a unit
-// is one (sequence, KV head, block of 8 NT query rows) -- lie end to end, and
-// every warp of the grid takes an equal run of them with a ring of its own in
-// shared memory: no barrier until the end.  A unit inside one warp's run is
-// written straight out.  Units cut by run ends leave (max, sum, partial
+// Work split: the tiles (32 tokens, 16 where rows are wide) of all units -- a
+// unit is one (sequence, KV head, block of 8 NT query rows) -- lie end to end,
+// and every warp of the grid takes an equal run of them with a ring of its own
+// in shared memory: no barrier until the end.  A unit inside one warp's run is
+// written straight out.  Units cut by run ends leave (exponent, sum, partial
 // output) pieces in the workspace; the CTA joins those of its warps, and for a
 // unit cut between CTAs the last one to arrive joins the CTAs' pieces, always
 // in order, so results do not depend on timing.
 #pragma once
-#include <cuda_bf16.h>
-
 #include <type_traits>
 
 #include "lkv_kernels.cuh"
@@ -50,16 +55,44 @@ namespace multi {
 
 using fused::hmma16816;
 using fused::hmma16816_bf16;
+using fused::hsub2_u32;
+using fused::kF16Magic2;
 
 constexpr unsigned kFull = 0xFFFFFFFFu;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr float kLazy = 8.0f;  // the running bound moves when a score passes it by 2^8
+constexpr float kLazy = 8.0f;      // the reference moves when a score passes it by 2^8
+constexpr int kTop = 7;            // scales are brought to at most 2^(kTop - 1): e * scale stays below 2^14
 
 __device__ __forceinline__ float ex2(float x) {  // 2^x; -inf gives 0
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// 2^n for an integer-valued n; 0 below the normal range.
+__device__ __forceinline__ float pow2i(float n) {
+  return n < -126.0f ? 0.0f : __uint_as_float((uint32_t)((int)fminf(n, 127.0f) + 127) << 23);
+}
+
+// tanh from its continued fraction x / (1 + x^2 / (3 + x^2 / (5 + ...))), cut
+// after the 13: relative error below 2e-7 up to |x| = 2.  Beyond, from the
+// exponential, where 2 / (1 + e^2x) is small and its error smaller still.
+__device__ __forceinline__ float tanh_near(float x) {
+  const float y = x * x;
+  const float num = fmaf(fmaf(y + 378.0f, y, 17325.0f), y, 135135.0f);
+  const float den = fmaf(fmaf(fmaf(28.0f, y, 3150.0f), y, 62370.0f), y, 135135.0f);
+  return x * num * rcp(den);
+}
+__device__ __forceinline__ float tanh_far(float x) {
+  const float t = 1.0f - 2.0f * rcp(1.0f + ex2(2.0f * kLog2e * fabsf(x)));
+  return copysignf(t, x);
 }
 
 // ------------------------------------------------------------------ the sequence side
@@ -72,7 +105,7 @@ struct Seq {
   int units;           // Hkv * row blocks
 };
 
-template <int NT>
+template <int NT, int TT>
 __device__ __forceinline__ Seq load_seq(const MultiArgs& a, int b) {
   Seq s;
   s.T = clamp_len(__ldg(a.lens + b), a.T_cap);
@@ -88,8 +121,8 @@ __device__ __forceinline__ Seq load_seq(const MultiArgs& a, int b) {
   int lo = s.start;
   if (a.window > 0) lo = max(lo, s.T - s.n - a.window + 1);
   s.lo = min(lo, s.T);
-  const int hi_t = (s.T + a.tt - 1) / a.tt, pre_t = (s.pre + a.tt - 1) / a.tt;
-  s.t_lo = s.lo / a.tt;
+  const int hi_t = (s.T + TT - 1) / TT, pre_t = (s.pre + TT - 1) / TT;
+  s.t_lo = s.lo / TT;
   s.np = min(pre_t, s.t_lo);
   s.cnt = max(1, s.np + max(0, hi_t - s.t_lo));  // a row that sees nothing still owns a tile: its zeros are written
   s.units = a.Hkv * ((s.n * a.r + 8 * NT - 1) / (8 * NT));
@@ -139,9 +172,10 @@ __device__ __forceinline__ void load_run(const uint8_t* p, int blk, int g, uint3
   }
 }
 
-__device__ __forceinline__ uint32_t bsub2(uint32_t a, uint32_t b) {
-  const __nv_bfloat162 r = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
-  return *reinterpret_cast<const uint32_t*>(&r);
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
 }
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
@@ -150,10 +184,19 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return r;
 }
 
-// Centred codes of two tokens (runs x, y) as bf16 pairs (x in the low half),
-// exact: out[c] for c = 0 .. CH-1.  Up to 6 bits a code is placed under the
-// pattern 0x4300 (128, unit spacing) and 128 + 2^(VB-1) subtracted; 8 bits go
-// through fp32 the same way; 16 bits are the values themselves.
+__device__ __forceinline__ float2 unpack_f16(uint32_t x) { return __half22float2(*reinterpret_cast<const __half2*>(&x)); }
+
+// Code c of a run stays at this bit of its half word (no shift below 10 bits of
+// mantissa): its MMA operand carries the factor 2^off, taken out at the end.
+template <int VB>
+constexpr int code_off(int c) {
+  return VB == 2 ? 2 * (c & 3) : VB == 4 ? 4 * (c & 1) : 0;
+}
+
+// Centred codes of two tokens (runs x, y) as fp16 pairs (x in the low half),
+// exact: out[c] = (code_c - 2^(VB-1)) * 2^off for c = 0 .. CH-1.  A code is
+// placed under the pattern 0x6400 (1024, unit spacing) and the pattern and the
+// middle subtracted at once; 16 bits are the bf16 values themselves.
 template <int VB, int CH>
 __device__ __forceinline__ void pair_codes(const uint32_t (&x)[VRun<VB, CH>::N], const uint32_t (&y)[VRun<VB, CH>::N],
                                            uint32_t (&out)[CH]) {
@@ -162,16 +205,13 @@ __device__ __forceinline__ void pair_codes(const uint32_t (&x)[VRun<VB, CH>::N],
     for (int c = 0; c < CH; ++c) out[c] = __byte_perm(x[c / 2], y[c / 2], (c & 1) ? 0x7632 : 0x5410);
   } else if constexpr (VB == 8) {
 #pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      const uint32_t sel = 0x7650u + (c & 3);  // bytes {code, 0, 0, 0x4B}
-      const float2 f = make_float2(__uint_as_float(__byte_perm(x[c / 4], 0x4B000000u, sel)),
-                                   __uint_as_float(__byte_perm(y[c / 4], 0x4B000000u, sel)));
-      const float2 d = __fadd2_rn(f, make_float2(-8388736.0f, -8388736.0f));
-      out[c] = pack_bf16(d.x, d.y);
+    for (int c = 0; c < CH; c += 2) {
+      const uint32_t z = __byte_perm(x[c / 4], y[c / 4], (c & 2) ? 0x7362 : 0x5140);  // {x, y, x', y'}
+      out[c] = hsub2_u32(__byte_perm(z, 0x64646464u, 0x4140), kF16Magic2 + 0x00800080u);
+      out[c + 1] = hsub2_u32(__byte_perm(z, 0x64646464u, 0x4342), kF16Magic2 + 0x00800080u);
     }
   } else {
     constexpr int cw = VB == 2 ? 8 : VB == 4 ? 4 : 2;  // codes of one 16-bit window
-    constexpr uint32_t mask = ((1u << VB) - 1u) * 0x00010001u;
 #pragma unroll
     for (int c0 = 0; c0 < CH; c0 += cw) {
       const int bit = c0 * VB, wi = bit / 32, sh = bit % 32;
@@ -183,98 +223,102 @@ __device__ __forceinline__ void pair_codes(const uint32_t (&x)[VRun<VB, CH>::N],
         z = __byte_perm(__funnelshift_r(x[wi], x[wn], sh), __funnelshift_r(y[wi], y[wn], sh), 0x5410);
       }
 #pragma unroll
-      for (int c = 0; c < cw && c0 + c < CH; ++c)
-        out[c0 + c] = bsub2(((z >> (c * VB)) & mask) | 0x43004300u, 0x43004300u + (1u << (VB - 1)) * 0x00010001u);
+      for (int c = 0; c < cw && c0 + c < CH; ++c) {
+        const int off = code_off<VB>(c);
+        const uint32_t mask = (((1u << VB) - 1u) << off) * 0x00010001u, mid = ((1u << (VB - 1)) << off) * 0x00010001u;
+        out[c0 + c] = hsub2_u32(((z >> (c * VB - off)) & mask) | kF16Magic2, kF16Magic2 + mid);
+      }
     }
   }
 }
 
-// ------------------------------------------------------------------ K codes
-// Register J of a lane's 16 codes: two centred codes as exact fp16 values
-// (c - 2^(KB-1)) * 2^off, by the extraction plan of mma_k.cuh.
-template <int KB, int J, int SW>
-__device__ __forceinline__ uint32_t k_reg(const uint32_t (&w)[SW]) {
-  if constexpr (KB == 16) {
-    return w[J];
-  } else {
-    using R = fused::RegChannels<KB, J>;
-    constexpr uint32_t mid = ((1u << (KB - 1)) << R::lo_off) | ((1u << (KB - 1)) << (16 + R::hi_off));
-    return fused::hsub2_u32(fused::a_reg_bits<KB, J, SW>(w), fused::kF16Magic2 + mid);
-  }
-}
-
-// The value of the middle code of a (scale, zero) pair.
-template <int BITS>
-__device__ __forceinline__ float centre(float scale, float zero) {
-  return fmaf((float)(1 << (BITS - 1)), scale, zero);
-}
-
 // ------------------------------------------------------------------ one warp's state
-template <int D, int NT, bool G32>
+template <int D_, int KB_, int VB_, int G_, int NT_>
+struct Cfg {
+  static constexpr int D = D_, KB = KB_, VB = VB_, G = G_, NT = NT_;
+  static constexpr int WARPS = shape_of(D_, KB_, VB_, G_, NT_).warps;
+  static constexpr int STAGES = shape_of(D_, KB_, VB_, G_, NT_).stages, STAGE = shape_of(D_, KB_, VB_, G_, NT_).stage;
+  static constexpr int OFF_KSZ = shape_of(D_, KB_, VB_, G_, NT_).off_ksz, OFF_VC = shape_of(D_, KB_, VB_, G_, NT_).off_vc;
+  static constexpr int OFF_VSZ = shape_of(D_, KB_, VB_, G_, NT_).off_vsz, SCRATCH = shape_of(D_, KB_, VB_, G_, NT_).scratch;
+  static constexpr int TT = shape_of(D_, KB_, VB_, G_, NT_).tt, TS = TT / 16;  // tokens of a tile, MMA tiles of it
+  static constexpr int BLK = D / 64;                // 64-channel blocks
+  static constexpr int MT = D / 16;                 // m-tiles of the output
+  static constexpr int NG = D / G;                  // groups
+  static constexpr int AC = KB == 16 ? 1 : NG;      // accumulators of a score: one per group
+  static constexpr int KRB = D * KB / 8, VRB = D * VB / 8;
+  // codes of a lane's V run: a run stays inside one group
+  static constexpr int CH = (G == 32 && VB != 16) ? 4 : 8;
+  static constexpr int RUNS = D / (8 * CH), TPB = CH / 2;  // runs of a row per lane, m-tiles of a run
+  static constexpr int GRUNS = VB == 16 ? RUNS : RUNS / NG;  // runs of one group
+};
+
+template <typename C>
 struct Work {
-  static constexpr int BLK = D / 64;                 // 64-channel blocks
-  static constexpr int MT = D / 16;                  // m-tiles of the output
-  static constexpr int NG = G32 ? D / 32 : D / 64;   // (scale, zero) slots; G = 128 reads slot 0 for both blocks
-  static constexpr int KG = G32 ? 2 : 1;             // K groups inside a 64-channel block
-  float o[MT][NT][4];
-  float zacc[NT][NG];   // sum of e * zero, this lane's tokens, row g
-  float m[NT], l[NT];   // running bound (base 2) and sum of e (this lane's tokens), row g
-  uint32_t qf[NT][BLK][8];
-  float ka[NT][2];            // factor of the code product, columns 2 tig and 2 tig + 1
-  float kz[NT][NG][2];        // the same times the sum of q over the group: the factor of zero
-  int p[NT], lo[NT];          // row g: position of its token, first visible token behind the prefix
-  float slope[NT];
-  bool on[NT];
-  // unit
-  int b, ui, g, rb, T, c0, n, pre, p_min, lo_max;
+  float o[C::MT][C::NT][4];
+  float zacc[C::NT][C::NG];   // sum of e * zero, this lane's tokens, row gid
+  float ref[C::NT], l[C::NT]; // reference exponent (an integer) and sum of e (this lane's tokens), row gid
+  bool live[C::NT];           // the row has seen a token
+  float refc[C::NT][2];       // references of columns 2 tig and 2 tig + 1 (0 when scores are capped)
+  float top;                  // o is in units of top * 2^-kTop, a power of two above the V scales seen
+  int orow[C::NT];            // row gid's place in out: row * Hq + head
+  uint32_t qf[C::NT][C::BLK][8];
+  float ka[C::NT][2];              // factor of the code product, columns 2 tig and 2 tig + 1
+  float kz[C::NT][C::NG][2];       // the same times the sum of q over the group: the factor of zero
+  int p[C::NT], lo[C::NT];         // row gid: position of its token, first visible token behind the prefix
+  float slope[C::NT];
+  bool on[C::NT];
+  int b, ui, g, rb, T, c0, n, pre, p_min, p_max, lo_min, lo_max;  // the unit
 };
 
 // q of the unit's rows as B fragments, and the factors of the affine part.
-template <int D, int NT, bool G32>
-__device__ __forceinline__ void load_unit(const MultiArgs& a, const Seq& s, int b, int ui, Work<D, NT, G32>& w) {
-  using W = Work<D, NT, G32>;
+template <typename C>
+__device__ __forceinline__ void load_unit(const MultiArgs& a, const Seq& s, int b, int ui, Work<C>& w) {
   const int lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
   const int rbs = s.units / a.Hkv;
   w.b = b; w.ui = ui; w.g = ui / rbs; w.rb = ui % rbs;
   w.T = s.T; w.c0 = s.c0; w.n = s.n; w.pre = s.pre;
-  const int r0 = w.rb * 8 * NT, r1 = min(r0 + 8 * NT, s.n * a.r);
-  // bounds that hold for every row of the block: a tile between them needs no mask
+  const int r0 = w.rb * 8 * C::NT, r1 = min(r0 + 8 * C::NT, s.n * a.r);
+  // what every row of the block sees, and what any row sees
   const int i0 = r0 / a.r, i1 = (r1 - 1) / a.r;
   w.p_min = s.T - s.n + i0;
-  w.lo_max = max(s.start, a.window > 0 ? s.T - s.n + i1 - a.window + 1 : 0);
+  w.p_max = s.T - s.n + i1;
+  w.lo_min = max(s.start, a.window > 0 ? w.p_min - a.window + 1 : 0);
+  w.lo_max = max(s.start, a.window > 0 ? w.p_max - a.window + 1 : 0);
+  w.top = pow2i(-126.0f + kTop);
 #pragma unroll
-  for (int mt = 0; mt < W::MT; ++mt)
+  for (int mt = 0; mt < C::MT; ++mt)
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int nt = 0; nt < C::NT; ++nt)
 #pragma unroll
       for (int i = 0; i < 4; ++i) w.o[mt][nt][i] = 0.0f;
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
+  for (int nt = 0; nt < C::NT; ++nt) {
     const int row = r0 + nt * 8 + gid;
     const int i = row / a.r, h = w.g * a.r + row % a.r;
     w.on[nt] = row < r1;
     w.p[nt] = s.T - s.n + i;
+    w.orow[nt] = (s.c0 + i) * a.Hq + h;
     w.lo[nt] = max(s.start, a.window > 0 ? w.p[nt] - a.window + 1 : 0);
     w.slope[nt] = w.on[nt] && a.slopes ? __ldg(a.slopes + h) * kLog2e : 0.0f;
-    w.m[nt] = -INFINITY;
-    w.l[nt] = 0.0f;
-    uint32_t raw[W::BLK][8];
+    w.ref[nt] = w.l[nt] = w.refc[nt][0] = w.refc[nt][1] = 0.0f;
+    w.live[nt] = false;
+    uint32_t raw[C::BLK][8];
 #pragma unroll
-    for (int blk = 0; blk < W::BLK; ++blk) {
+    for (int blk = 0; blk < C::BLK; ++blk) {
       uint4 u = make_uint4(0, 0, 0, 0), v = u;
       if (w.on[nt]) {
-        const uint4* src = reinterpret_cast<const uint4*>(a.q + ((long long)(s.c0 + i) * a.Hq + h) * D + blk * 64 + tig * 16);
+        const uint4* src = reinterpret_cast<const uint4*>(a.q + ((long long)(s.c0 + i) * a.Hq + h) * C::D + blk * 64 + tig * 16);
         u = __ldg(src); v = __ldg(src + 1);
       }
       raw[blk][0] = u.x; raw[blk][1] = u.y; raw[blk][2] = u.z; raw[blk][3] = u.w;
       raw[blk][4] = v.x; raw[blk][5] = v.y; raw[blk][6] = v.z; raw[blk][7] = v.w;
     }
     // sums of q over each group, and its largest magnitude
-    float big = 0.0f, sum[W::NG];
+    float big = 0.0f, sum[C::NG];
 #pragma unroll
-    for (int gi = 0; gi < W::NG; ++gi) { sum[gi] = 0.0f; w.zacc[nt][gi] = 0.0f; }
+    for (int gi = 0; gi < C::NG; ++gi) sum[gi] = w.zacc[nt][gi] = 0.0f;
 #pragma unroll
-    for (int blk = 0; blk < W::BLK; ++blk) {
+    for (int blk = 0; blk < C::BLK; ++blk) {
       float t = 0.0f;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
@@ -283,22 +327,21 @@ __device__ __forceinline__ void load_unit(const MultiArgs& a, const Seq& s, int 
         big = fmaxf(big, fmaxf(fabsf(x), fabsf(y)));
       }
       t += __shfl_xor_sync(kFull, t, 1);
-      if constexpr (G32) {
-        const float other = __shfl_xor_sync(kFull, t, 2);
+      const float other = __shfl_xor_sync(kFull, t, 2);
+      if constexpr (C::G == 32) {
         sum[2 * blk] = tig < 2 ? t : other;
         sum[2 * blk + 1] = tig < 2 ? other : t;
       } else {
-        t += __shfl_xor_sync(kFull, t, 2);
-        sum[blk] = t;
+        sum[blk * C::NG / C::BLK] += t + other;
       }
     }
     big = fmaxf(big, __shfl_xor_sync(kFull, big, 1));
     big = fmaxf(big, __shfl_xor_sync(kFull, big, 2));
-    float unit = a.softcap > 0.0f ? a.scale / a.softcap : a.scale * kLog2e;
+    const float unit = a.softcap > 0.0f ? a.scale / a.softcap : a.scale * kLog2e;
     float back = unit;
-    if (a.kb == 16) {
+    if constexpr (C::KB == 16) {
 #pragma unroll
-      for (int blk = 0; blk < W::BLK; ++blk)
+      for (int blk = 0; blk < C::BLK; ++blk)
 #pragma unroll
         for (int j = 0; j < 8; ++j) w.qf[nt][blk][j] = raw[blk][j];
     } else {
@@ -308,19 +351,14 @@ __device__ __forceinline__ void load_unit(const MultiArgs& a, const Seq& s, int 
       const float up = __uint_as_float((uint32_t)(e + 127) << 23), down = __uint_as_float((uint32_t)(127 - e) << 23);
       back = unit * down;
 #pragma unroll
-      for (int blk = 0; blk < W::BLK; ++blk) {
+      for (int blk = 0; blk < C::BLK; ++blk) {
         __half qh[16];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           qh[2 * j] = __float2half_rn(bf16_lo(raw[blk][j]) * up);
           qh[2 * j + 1] = __float2half_rn(bf16_hi(raw[blk][j]) * up);
         }
-        switch (a.kb) {
-          case 2: fused::bfrag_one<2, 64, 0>(qh, 0, true, w.qf[nt][blk]); break;
-          case 4: fused::bfrag_one<4, 64, 0>(qh, 0, true, w.qf[nt][blk]); break;
-          case 6: fused::bfrag_one<6, 64, 0>(qh, 0, true, w.qf[nt][blk]); break;
-          default: fused::bfrag_one<8, 64, 0>(qh, 0, true, w.qf[nt][blk]); break;
-        }
+        fused::bfrag_one<C::KB, 64, 0>(qh, 0, true, w.qf[nt][blk]);
       }
     }
     // the K product leaves columns 2 tig and 2 tig + 1 in this lane
@@ -329,23 +367,138 @@ __device__ __forceinline__ void load_unit(const MultiArgs& a, const Seq& s, int 
       const int src = 4 * (2 * tig + j);
       w.ka[nt][j] = __shfl_sync(kFull, back, src);
 #pragma unroll
-      for (int gi = 0; gi < W::NG; ++gi) w.kz[nt][gi][j] = unit * __shfl_sync(kFull, sum[gi], src);
+      for (int gi = 0; gi < C::NG; ++gi) w.kz[nt][gi][j] = unit * __shfl_sync(kFull, sum[gi], src);
     }
   }
 }
 
-// ------------------------------------------------------------------ scores of 16 tokens
-// acc[blk * KG + half][nt] += K codes (rows = tokens t0 + gid, t0 + gid + 8) x q.
-template <int KB, int D, int NT, bool G32>
-__device__ __forceinline__ void k_product(const uint8_t* kc, const Work<D, NT, G32>& w,
-                                          float (&acc)[Work<D, NT, G32>::BLK * Work<D, NT, G32>::KG][NT][4]) {
-  using W = Work<D, NT, G32>;
-  constexpr int RB = D * KB / 8, SW = KB / 2;  // row bytes, words of a lane's 16 codes
-  const int lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
+// ------------------------------------------------------------------ what a token brings
+// Per warp: transposed scores, and the constants that take each token's K
+// centre out of the codes.
+template <typename C>
+struct Scratch {
+  static constexpr int kScores = C::TT * 8 * C::NT;  // floats
+  static constexpr int kBytes = kScores * 4 + C::TT * C::NG * centre_words(C::KB) * 4;
+};
+
+// The fp16 pattern of two codes at bits (lo, hi) of their half words holds
+// 1024 + c 2^off; less 1024 + centre 2^off it is the centred code.  Which of a
+// token's constants that is: at 6 and 4 bits one for each pair of offsets in
+// the plan of mma_k.cuh, else the centre itself.
+template <int KB>
+constexpr int centre_index(int lo) {
+  return KB == 6 ? (lo == 0 ? 0 : lo == 1 ? 1 : lo == 4 ? 2 : 3) : KB == 4 ? (lo == 0 ? 0 : 1) : 0;
+}
+constexpr uint32_t centre_mul(int lo, int hi) { return (1u << lo) | (1u << (16 + hi)); }
+
+constexpr float kRound = 12582912.0f;       // 1.5 * 2^23: adding it rounds to an integer in the low bits
+constexpr uint32_t kRoundBits = 0x4B400000u;
+
+// The lane of a token readies its (scale, zero) rows: K's zero becomes the
+// value of the code nearest 0 (the code itself goes to cen), V's that of the middle code, and V's scale is taken relative
+// to w.top, which is raised (and the output rescaled) when a scale passes it.
+// What no row sees becomes 0 in V.
+template <typename C>
+__device__ __forceinline__ void ready_tokens(Work<C>& w, uint8_t* stage, uint32_t* cen, int t0, bool whole) {
+  const int lane = threadIdx.x & 31;
+  const bool mine = C::TT == 32 || lane < C::TT;
+  const int t = t0 + lane;
+  const bool alive = whole || (t < w.T && (t < w.pre || (t >= w.lo_min && t <= w.p_max)));
+  if constexpr (C::KB < 16) {
+    float* ksz = reinterpret_cast<float*>(stage + C::OFF_KSZ) + lane * C::NG * 2;
+    if (mine) {
 #pragma unroll
-  for (int blk = 0; blk < W::BLK; ++blk) {
+      for (int gi = 0; gi < C::NG; ++gi) {
+        const float2 v = *reinterpret_cast<const float2*>(ksz + 2 * gi);
+        const float c = fminf(fmaxf(-v.y * rcp(v.x), 0.0f), (float)((1 << C::KB) - 1)) + kRound;
+        constexpr int CW = centre_words(C::KB);
+        uint32_t* to = cen + (lane * C::NG + gi) * CW;
+        const uint32_t n = __float_as_uint(c) - kRoundBits;
+        if constexpr (C::KB == 6) {
+          *reinterpret_cast<uint4*>(to) = make_uint4(n * centre_mul(0, 2) + kF16Magic2, n * centre_mul(1, 3) + kF16Magic2,
+                                                     n * centre_mul(4, 0) + kF16Magic2, n * centre_mul(2, 4) + kF16Magic2);
+        } else if constexpr (C::KB == 4) {
+          *reinterpret_cast<uint2*>(to) = make_uint2(n * centre_mul(0, 0) + kF16Magic2, n * centre_mul(4, 4) + kF16Magic2);
+        } else {
+          to[0] = n;
+        }
+        ksz[2 * gi + 1] = fmaf(c - kRound, v.x, v.y);
+      }
+    }
+  }
+  if constexpr (C::VB < 16) {
+    float* vsz = reinterpret_cast<float*>(stage + C::OFF_VSZ) + lane * C::NG * 2;
+    float2 v[C::NG];
+    float big = 0.0f;
+#pragma unroll
+    for (int gi = 0; gi < C::NG; ++gi) {
+      v[gi] = make_float2(0.0f, 0.0f);
+      if (mine && alive) v[gi] = *reinterpret_cast<const float2*>(vsz + 2 * gi);
+      big = fmaxf(big, v[gi].x);
+    }
+    if (__any_sync(kFull, big > w.top)) {
+#pragma unroll
+      for (int off = 16; off >= 1; off >>= 1) big = fmaxf(big, __shfl_xor_sync(kFull, big, off));
+      // a power of two at least twice as large
+      const float top = pow2i((float)((int)(__float_as_uint(big) >> 23) - 127 + 2)), f = w.top * (1.0f / top);
+      w.top = top;
+#pragma unroll
+      for (int mt = 0; mt < C::MT; ++mt)
+#pragma unroll
+        for (int nt = 0; nt < C::NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) w.o[mt][nt][i] *= f;
+    }
+    const float rel = (float)(1 << kTop) / w.top;
+    if (mine) {
+#pragma unroll
+      for (int gi = 0; gi < C::NG; ++gi)
+        *reinterpret_cast<float2*>(vsz + 2 * gi) = make_float2(v[gi].x * rel, fmaf((float)(1 << (C::VB - 1)), v[gi].x, v[gi].y));
+    }
+  } else if (!whole) {
+    unsigned gone = __ballot_sync(kFull, mine && !alive);
+    while (gone) {
+      const int r = __ffs(gone) - 1;
+      gone &= gone - 1;
+      uint8_t* row = stage + C::OFF_VC + r * C::VRB;
+#pragma unroll
+      for (int i = 0; i < C::VRB / 128; ++i) reinterpret_cast<uint32_t*>(row)[lane + 32 * i] = 0u;
+    }
+  }
+  __syncwarp();
+}
+
+// ------------------------------------------------------------------ scores
+// Register J of a lane's 16 codes: two codes less the centre as exact fp16
+// values times 2^off, by the extraction plan of mma_k.cuh; at 16 bits the two
+// bf16 values.
+template <int KB, int J>
+__device__ __forceinline__ uint32_t k_reg(const uint32_t (&word)[KB / 2], const uint32_t (&cen)[4]) {
+  if constexpr (KB == 16) {
+    return word[J];
+  } else {
+    using R = fused::RegChannels<KB, J>;
+    constexpr int i = centre_index<KB>(R::lo_off);
+    static_assert(KB != 6 || centre_mul(R::lo_off, R::hi_off) == (i == 0 ? centre_mul(0, 2) : i == 1 ? centre_mul(1, 3) : i == 2 ? centre_mul(4, 0) : centre_mul(2, 4)),
+                  "a constant for each pair of offsets");
+    static_assert(KB != 4 || centre_mul(R::lo_off, R::hi_off) == (i == 0 ? centre_mul(0, 0) : centre_mul(4, 4)), "and at 4 bits");
+    uint32_t k = cen[i];
+    if constexpr (centre_words(KB) == 1) k = k * centre_mul(R::lo_off, R::hi_off) + kF16Magic2;
+    return hsub2_u32(fused::a_reg_bits<KB, J, KB / 2>(word), k);
+  }
+}
+
+// acc[ts][group][nt] += K codes (rows = tokens 16 ts + gid, + 8) x q.
+template <typename C>
+__device__ __forceinline__ void k_product(const uint8_t* kc, const uint32_t* cen, const Work<C>& w, int ts,
+                                          float (&acc)[C::AC][C::NT][4]) {
+  constexpr int KB = C::KB, RB = C::KRB, SW = KB / 2;  // row bytes, words of a lane's 16 codes
+  const int lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
+  const uint8_t* base = kc + (16 * ts + gid) * RB + tig * 2 * KB;
+#pragma unroll
+  for (int blk = 0; blk < C::BLK; ++blk) {
     uint32_t x[SW], y[SW];
-    const uint8_t* p = kc + gid * RB + blk * 8 * KB + tig * 2 * KB;
+    const uint8_t* p = base + blk * 8 * KB;
     if constexpr (SW % 4 == 0) {
 #pragma unroll
       for (int i = 0; i < SW; i += 4) {
@@ -363,17 +516,34 @@ __device__ __forceinline__ void k_product(const uint8_t* kc, const Work<D, NT, G
         y[i] = *reinterpret_cast<const uint32_t*>(p + 8 * RB + 4 * i);
       }
     }
+    uint32_t cx[4] = {0, 0, 0, 0}, cy[4] = {0, 0, 0, 0};
+    if constexpr (KB < 16) {
+      // the lane's codes lie in one group: its half of the block at G = 32
+      constexpr int CW = centre_words(KB);
+      const int gi = C::G == 32 ? 2 * blk + (tig >> 1) : blk * C::NG / C::BLK;
+      const uint32_t *px = cen + ((16 * ts + gid) * C::NG + gi) * CW, *py = px + 8 * C::NG * CW;
+      if constexpr (CW == 4) {
+        const uint4 u = *reinterpret_cast<const uint4*>(px), v = *reinterpret_cast<const uint4*>(py);
+        cx[0] = u.x; cx[1] = u.y; cx[2] = u.z; cx[3] = u.w;
+        cy[0] = v.x; cy[1] = v.y; cy[2] = v.z; cy[3] = v.w;
+      } else if constexpr (CW == 2) {
+        const uint2 u = *reinterpret_cast<const uint2*>(px), v = *reinterpret_cast<const uint2*>(py);
+        cx[0] = u.x; cx[1] = u.y; cy[0] = v.x; cy[1] = v.y;
+      } else {
+        cx[0] = *px; cy[0] = *py;
+      }
+    }
     auto step = [&](auto ks_c) {
       constexpr int ks = decltype(ks_c)::value;
-      const uint32_t a0 = k_reg<KB, 2 * ks, SW>(x), a1 = k_reg<KB, 2 * ks, SW>(y);
-      const uint32_t a2 = k_reg<KB, 2 * ks + 1, SW>(x), a3 = k_reg<KB, 2 * ks + 1, SW>(y);
+      const uint32_t a0 = k_reg<KB, 2 * ks>(x, cx), a1 = k_reg<KB, 2 * ks>(y, cy);
+      const uint32_t a2 = k_reg<KB, 2 * ks + 1>(x, cx), a3 = k_reg<KB, 2 * ks + 1>(y, cy);
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
+      for (int nt = 0; nt < C::NT; ++nt) {
         const uint32_t b0 = w.qf[nt][blk][2 * ks], b1 = w.qf[nt][blk][2 * ks + 1];
         if constexpr (KB == 16) {
-          hmma16816_bf16(acc[blk * W::KG][nt], a0, a1, a2, a3, b0, b1);
-        } else if constexpr (!G32) {
-          hmma16816(acc[blk][nt], a0, a1, a2, a3, b0, b1);
+          hmma16816_bf16(acc[0][nt], a0, a1, a2, a3, b0, b1);
+        } else if constexpr (C::G != 32) {
+          hmma16816(acc[blk * C::NG / C::BLK][nt], a0, a1, a2, a3, b0, b1);
         } else {
           // lanes tig < 2 hold the block's first group of 32 channels, the others its second
           hmma16816(acc[2 * blk][nt], a0, a1, a2, a3, tig < 2 ? b0 : 0u, tig < 2 ? b1 : 0u);
@@ -388,252 +558,264 @@ __device__ __forceinline__ void k_product(const uint8_t* kc, const Work<D, NT, G
   }
 }
 
-// out += sum over the 16 tokens of (e * scale) code: rows = channels, slots
-// 2 tig, 2 tig + 1, 2 tig + 8, 2 tig + 9 = tokens tig, tig + 4, tig + 8, tig + 12.
-// dead: bit j set when no row of the unit sees token tig + 4 j (its 16-bit
-// values may be anything and are taken as zero; codes are finite as they are).
-template <int VB, int D, int NT, bool G32>
-__device__ __forceinline__ void v_product(const uint8_t* vc, const float* vsz, int ng, Work<D, NT, G32>& w,
-                                          const float (&e)[NT][4], const unsigned (&seen)[NT], unsigned dead) {
-  using W = Work<D, NT, G32>;
-  constexpr int RB = D * VB / 8;
-  constexpr int CH = (G32 && VB != 16) ? 4 : 8;  // codes of a lane's run; a run stays inside one group
-  constexpr int NB = D / (8 * CH), TPB = CH / 2; // runs of a row per lane, m-tiles of a run
-  constexpr int N = VRun<VB, CH>::N;
+// ------------------------------------------------------------------ output
+// o += sum over 16 tokens of (e * scale) code: rows = channels, slots 2 tig,
+// 2 tig + 1, 2 tig + 8, 2 tig + 9 = tokens tig, tig + 4, tig + 8, tig + 12.
+template <typename C>
+__device__ __forceinline__ void v_product(const uint8_t* vc, const float* vsz, Work<C>& w, int ts, const float (&e)[C::NT][4]) {
+  constexpr int VB = C::VB, CH = C::CH, N = VRun<VB, CH>::N;
   const int lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
-  const int per = D / (8 * CH) / (VB == 16 ? 1 : ng);  // runs of one group
-  uint32_t hi[NT][2], lo[NT][2];
+  const uint8_t* base = vc + (16 * ts + tig) * C::VRB;
+  const float* szb = vsz + (16 * ts + tig) * C::NG * 2;
+  constexpr int TERMS = VB == 16 ? 3 : 2;
+  uint32_t pw[C::NT][TERMS][2];
 #pragma unroll
-  for (int blk = 0; blk < NB; ++blk) {
-    const bool fresh = VB == 16 ? blk == 0 : blk % per == 0;
-    if (fresh) {
-      float sc[4], ze[4];
-      if constexpr (VB != 16) {
+  for (int run = 0; run < C::RUNS; ++run) {
+    if (run % C::GRUNS == 0) {
+      const int gi = run / C::GRUNS;
+      float2 sz[4];
+      if constexpr (VB < 16) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 t = *reinterpret_cast<const float2*>(vsz + ((tig + 4 * j) * ng + blk / per) * 2);
-          sc[j] = t.x; ze[j] = centre<VB>(t.x, t.y);
-        }
+        for (int j = 0; j < 4; ++j) sz[j] = *reinterpret_cast<const float2*>(szb + (4 * j * C::NG + gi) * 2);
       }
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float x[4];
+      for (int nt = 0; nt < C::NT; ++nt) {
+        if constexpr (VB == 16) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if constexpr (VB == 16) {
-            x[j] = e[nt][j];
-          } else {
-            // a row that does not see the token must not meet its (scale, zero): they may be anything
-            const bool ok = seen[nt] >> j & 1;
-            x[j] = ok ? e[nt][j] * sc[j] : 0.0f;
-            if (ok) w.zacc[nt][blk / (NB / W::NG)] += e[nt][j] * ze[j];
+          for (int j = 0; j < 2; ++j) {
+            const float x = e[nt][2 * j], y = e[nt][2 * j + 1];
+            const uint32_t h = pack_bf16(x, y);
+            const float xr = x - bf16_lo(h), yr = y - bf16_hi(h);
+            const uint32_t m = pack_bf16(xr, yr);
+            pw[nt][0][j] = h;
+            pw[nt][1][j] = m;
+            pw[nt][2][j] = pack_bf16(xr - bf16_lo(m), yr - bf16_hi(m));
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const float x = e[nt][2 * j] * sz[2 * j].x, y = e[nt][2 * j + 1] * sz[2 * j + 1].x;
+            w.zacc[nt][gi] = fmaf(e[nt][2 * j], sz[2 * j].y, fmaf(e[nt][2 * j + 1], sz[2 * j + 1].y, w.zacc[nt][gi]));
+            const uint32_t h = pack_f16(x, y);
+            const float2 f = unpack_f16(h);
+            pw[nt][0][j] = h;
+            pw[nt][1][j] = pack_f16(x - f.x, y - f.y);
           }
         }
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          hi[nt][j] = pack_bf16(x[2 * j], x[2 * j + 1]);
-          lo[nt][j] = pack_bf16(x[2 * j] - bf16_lo(hi[nt][j]), x[2 * j + 1] - bf16_hi(hi[nt][j]));
-        }
       }
     }
-    uint32_t run[4][N];
+    uint32_t r[4][N];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) load_run<VB, CH>(vc + (tig + 4 * j) * RB, blk, gid, run[j]);
-    if constexpr (VB == 16) {
-      if (dead) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-          for (int i = 0; i < N; ++i) run[j][i] = dead >> j & 1 ? 0u : run[j][i];
-      }
-    }
+    for (int j = 0; j < 4; ++j) load_run<VB, CH>(base + 4 * j * C::VRB, run, gid, r[j]);
     uint32_t u[CH], v[CH];
-    pair_codes<VB, CH>(run[0], run[1], u);
-    pair_codes<VB, CH>(run[2], run[3], v);
+    pair_codes<VB, CH>(r[0], r[1], u);
+    pair_codes<VB, CH>(r[2], r[3], v);
 #pragma unroll
-    for (int mi = 0; mi < TPB; ++mi)
+    for (int term = 0; term < TERMS; ++term)
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        hmma16816_bf16(w.o[blk * TPB + mi][nt], u[2 * mi], u[2 * mi + 1], v[2 * mi], v[2 * mi + 1], hi[nt][0], hi[nt][1]);
-        hmma16816_bf16(w.o[blk * TPB + mi][nt], u[2 * mi], u[2 * mi + 1], v[2 * mi], v[2 * mi + 1], lo[nt][0], lo[nt][1]);
-      }
+      for (int mi = 0; mi < C::TPB; ++mi)
+#pragma unroll
+        for (int nt = 0; nt < C::NT; ++nt) {
+          float(&o)[4] = w.o[run * C::TPB + mi][nt];
+          if constexpr (VB == 16) {
+            hmma16816_bf16(o, u[2 * mi], u[2 * mi + 1], v[2 * mi], v[2 * mi + 1], pw[nt][term][0], pw[nt][term][1]);
+          } else {
+            hmma16816(o, u[2 * mi], u[2 * mi + 1], v[2 * mi], v[2 * mi + 1], pw[nt][term][0], pw[nt][term][1]);
+          }
+        }
   }
 }
 
-// Channel of output register (mt, half) for lane gid: runs of CH channels.
-template <int D, bool G32>
-__device__ __forceinline__ int out_channel(int mt, int half, int gid, bool wide) {
-  if (G32 && !wide) return (mt / 2) * 32 + gid * 4 + (mt % 2) * 2 + half;
-  return (mt / 4) * 64 + gid * 8 + (mt % 4) * 2 + half;
-}
-
-// 16 tokens from position t0 (n of them staged): scores, running softmax, output.
-template <int D, int NT, bool G32>
-__device__ __forceinline__ void step16(const MultiArgs& a, Work<D, NT, G32>& w, const uint8_t* kc, const float* ksz,
-                                       const uint8_t* vc, const float* vsz, float* tr, int t0, int ng) {
-  using W = Work<D, NT, G32>;
+// One staged tile from position t0: scores, running softmax, output.
+template <typename C>
+__device__ __forceinline__ void tile_step(const MultiArgs& a, Work<C>& w, uint8_t* stage, float* tr, int t0) {
+  constexpr int TS = C::TS, NT = C::NT, NG = C::NG;
   const int lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
-  float acc[W::BLK * W::KG][NT][4];
+  uint32_t* cen = reinterpret_cast<uint32_t*>(tr + Scratch<C>::kScores);
+  const float* ksz = reinterpret_cast<const float*>(stage + C::OFF_KSZ);
+  const float* vsz = reinterpret_cast<const float*>(stage + C::OFF_VSZ);
+  const int t1 = t0 + C::TT - 1;
+  const bool whole = t1 < w.T && ((t0 >= w.lo_max && t1 <= w.p_min) || t1 < w.pre);
+  ready_tokens<C>(w, stage, cen, t0, whole);
 #pragma unroll
-  for (int i = 0; i < W::BLK * W::KG; ++i)
+  for (int ts = 0; ts < TS; ++ts) {
+    float acc[C::AC][NT][4];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int i = 0; i < C::AC; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) acc[i][nt][j] = 0.0f;
-  switch (a.kb) {
-    case 2: k_product<2, D, NT, G32>(kc, w, acc); break;
-    case 4: k_product<4, D, NT, G32>(kc, w, acc); break;
-    case 6: k_product<6, D, NT, G32>(kc, w, acc); break;
-    case 8: k_product<8, D, NT, G32>(kc, w, acc); break;
-    default: k_product<16, D, NT, G32>(kc, w, acc); break;
-  }
-  // fold (scale, zero): rows gid and gid + 8, columns 2 tig and 2 tig + 1
-  float s[NT][4];
-  if (a.kb == 16) {
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+        for (int j = 0; j < 4; ++j) acc[i][nt][j] = 0.0f;
+    k_product<C>(stage, cen, w, ts, acc);
+    // fold (scale, zero): rows gid and gid + 8, columns 2 tig and 2 tig + 1.  The
+    // reference goes in before the one large rounding, so the scores that
+    // matter, those near it, are rounded at their small distance from it.
+    float s[NT][4];
+    if constexpr (C::KB == 16) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        float t = acc[0][nt][j];
-        if constexpr (W::BLK == 2) t += acc[W::KG][nt][j];
-        s[nt][j] = t * w.ka[nt][j & 1];
-      }
-  } else {
-    float sc[2][W::NG], ze[2][W::NG];
-    const float mid = (float)(1 << (a.kb - 1));
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+        for (int j = 0; j < 4; ++j) s[nt][j] = fmaf(acc[0][nt][j], w.ka[nt][j & 1], -w.refc[nt][j & 1]);
+    } else {
+      float2 sz[2][NG];
 #pragma unroll
-      for (int gi = 0; gi < W::NG; ++gi) {
-        const float2 t = *reinterpret_cast<const float2*>(ksz + ((gid + 8 * i) * ng + gi * ng / W::NG) * 2);
-        sc[i][gi] = t.x; ze[i][gi] = fmaf(mid, t.x, t.y);
-      }
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+        for (int gi = 0; gi < NG; ++gi) sz[i][gi] = *reinterpret_cast<const float2*>(ksz + ((16 * ts + gid + 8 * i) * NG + gi) * 2);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        float t = sc[j >> 1][0] * acc[0][nt][j];
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int gi = 1; gi < W::NG; ++gi) t = fmaf(sc[j >> 1][gi], acc[gi][nt][j], t);
-        float z = ze[j >> 1][0] * w.kz[nt][0][j & 1];
+        for (int j = 0; j < 4; ++j) {
+          float t = sz[j >> 1][0].x * acc[0][nt][j], z = -w.refc[nt][j & 1];
 #pragma unroll
-        for (int gi = 1; gi < W::NG; ++gi) z = fmaf(ze[j >> 1][gi], w.kz[nt][gi][j & 1], z);
-        s[nt][j] = fmaf(t, w.ka[nt][j & 1], z);
-      }
-  }
-  // transpose through shared memory: lane (gid, tig) takes row gid, tokens tig + 4 j
+          for (int gi = 1; gi < NG; ++gi) t = fmaf(sz[j >> 1][gi].x, acc[gi][nt][j], t);
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    *reinterpret_cast<float2*>(tr + nt * 128 + gid * 8 + 2 * tig) = make_float2(s[nt][0], s[nt][1]);
-    *reinterpret_cast<float2*>(tr + nt * 128 + (gid + 8) * 8 + 2 * tig) = make_float2(s[nt][2], s[nt][3]);
+          for (int gi = 0; gi < NG; ++gi) z = fmaf(sz[j >> 1][gi].y, w.kz[nt][gi][j & 1], z);
+          s[nt][j] = fmaf(t, w.ka[nt][j & 1], z);
+        }
+    }
+    // transpose through shared memory: lane (gid, tig) takes row gid, tokens tig + 4 j
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      float* dst = tr + (ts * NT + nt) * 128 + gid * 8 + 2 * tig;
+      *reinterpret_cast<float2*>(dst) = make_float2(s[nt][0], s[nt][1]);
+      *reinterpret_cast<float2*>(dst + 64) = make_float2(s[nt][2], s[nt][3]);
+    }
   }
   __syncwarp();
-  float e[NT][4];
+  float e[TS][NT][4];
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
+  for (int ts = 0; ts < TS; ++ts)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) e[nt][j] = tr[nt * 128 + (tig + 4 * j) * 8 + gid];
-  __syncwarp();
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) e[ts][nt][j] = tr[(ts * NT + nt) * 128 + (tig + 4 * j) * 8 + gid];
   if (a.softcap > 0.0f) {
     const float c = a.softcap * kLog2e;
+    bool far = false;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int ts = 0; ts < TS; ++ts)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) e[nt][j] = c * tanhf(e[nt][j]);
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) far |= fabsf(e[ts][nt][j]) > 2.0f;
+    if (__any_sync(kFull, far)) {
+#pragma unroll
+      for (int ts = 0; ts < TS; ++ts)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float x = e[ts][nt][j];
+            e[ts][nt][j] = fmaf(c, fabsf(x) > 2.0f ? tanh_far(x) : tanh_near(x), -w.ref[nt]);
+          }
+    } else {
+#pragma unroll
+      for (int ts = 0; ts < TS; ++ts)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) e[ts][nt][j] = fmaf(c, tanh_near(e[ts][nt][j]), -w.ref[nt]);
+    }
   }
   if (a.slopes != nullptr) {
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int ts = 0; ts < TS; ++ts)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) e[nt][j] = fmaf(w.slope[nt], (float)(t0 + tig + 4 * j - w.p[nt]), e[nt][j]);
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          e[ts][nt][j] = fmaf(w.slope[nt], (float)(t0 + 16 * ts + tig + 4 * j - w.p[nt]), e[ts][nt][j]);
   }
-  const bool whole = t0 + 15 < w.T && ((t0 >= w.lo_max && t0 + 15 <= w.p_min) || t0 + 15 < w.pre);
-  unsigned seen[NT], dead = 0;
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) seen[nt] = w.on[nt] ? 15u : 0u;
   if (!whole) {
-    unsigned any = 0;
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int ts = 0; ts < TS; ++ts)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int t = t0 + tig + 4 * j;
-        const bool ok = w.on[nt] && t < w.T && (t < w.pre || (t >= w.lo[nt] && t <= w.p[nt]));
-        if (!ok) seen[nt] &= ~(1u << j);
-        if (ok) any |= 1u << j;
-      }
-    // seen by any row of the unit: over the lanes of the same tig
-    any |= __shfl_xor_sync(kFull, any, 4);
-    any |= __shfl_xor_sync(kFull, any, 8);
-    any |= __shfl_xor_sync(kFull, any, 16);
-    dead = ~any & 15u;
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int t = t0 + 16 * ts + tig + 4 * j;
+          if (!(t < w.T && (t < w.pre || (t >= w.lo[nt] && t <= w.p[nt])))) e[ts][nt][j] = -INFINITY;
+        }
   }
   float mx[NT];
   bool grow = false;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
+    float t = -INFINITY;
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (!(seen[nt] >> j & 1)) e[nt][j] = -INFINITY;
-    float t = fmaxf(fmaxf(e[nt][0], e[nt][1]), fmaxf(e[nt][2], e[nt][3]));
+    for (int ts = 0; ts < TS; ++ts)
+      t = fmaxf(t, fmaxf(fmaxf(e[ts][nt][0], e[ts][nt][1]), fmaxf(e[ts][nt][2], e[ts][nt][3])));
     t = fmaxf(t, __shfl_xor_sync(kFull, t, 1));
     t = fmaxf(t, __shfl_xor_sync(kFull, t, 2));
     mx[nt] = t;
-    grow |= t > w.m[nt] + kLazy;  // from -inf: any finite score
+    grow |= t > (w.live[nt] ? kLazy : -INFINITY);
   }
   if (__any_sync(kFull, grow)) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      const float m = fmaxf(w.m[nt], mx[nt]);
-      const float al = m == -INFINITY ? 1.0f : ex2(w.m[nt] - m);
-      w.m[nt] = m;
+      const bool any = mx[nt] > -INFINITY;
+      const float most = any ? ceilf(mx[nt] + w.ref[nt]) : w.ref[nt];
+      const float ref = w.live[nt] ? fmaxf(w.ref[nt], most) : most;
+      w.live[nt] |= any;
+      const float by = ref - w.ref[nt], al = pow2i(-by);
+      w.ref[nt] = ref;
       w.l[nt] *= al;
 #pragma unroll
-      for (int gi = 0; gi < W::NG; ++gi) w.zacc[nt][gi] *= al;
-      const float a0 = __shfl_sync(kFull, al, 8 * tig), a1 = __shfl_sync(kFull, al, 8 * tig + 4);
+      for (int gi = 0; gi < NG; ++gi) w.zacc[nt][gi] *= al;
 #pragma unroll
-      for (int mt = 0; mt < W::MT; ++mt) {
+      for (int ts = 0; ts < TS; ++ts)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) e[ts][nt][j] -= by;
+      const float a0 = __shfl_sync(kFull, al, 8 * tig), a1 = __shfl_sync(kFull, al, 8 * tig + 4);
+      const float r0 = __shfl_sync(kFull, ref, 8 * tig), r1 = __shfl_sync(kFull, ref, 8 * tig + 4);
+      if (a.softcap <= 0.0f) { w.refc[nt][0] = r0; w.refc[nt][1] = r1; }
+#pragma unroll
+      for (int mt = 0; mt < C::MT; ++mt) {
         w.o[mt][nt][0] *= a0; w.o[mt][nt][1] *= a1;
         w.o[mt][nt][2] *= a0; w.o[mt][nt][3] *= a1;
       }
     }
   }
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    const float m = w.m[nt] == -INFINITY ? 0.0f : w.m[nt];
+  for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) e[nt][j] = ex2(e[nt][j] - m);
-    w.l[nt] += (e[nt][0] + e[nt][1]) + (e[nt][2] + e[nt][3]);
-  }
-  switch (a.vb) {
-    case 2: v_product<2, D, NT, G32>(vc, vsz, ng, w, e, seen, dead); break;
-    case 4: v_product<4, D, NT, G32>(vc, vsz, ng, w, e, seen, dead); break;
-    case 6: v_product<6, D, NT, G32>(vc, vsz, ng, w, e, seen, dead); break;
-    case 8: v_product<8, D, NT, G32>(vc, vsz, ng, w, e, seen, dead); break;
-    default: v_product<16, D, NT, G32>(vc, vsz, ng, w, e, seen, dead); break;
-  }
+    for (int ts = 0; ts < TS; ++ts) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) e[ts][nt][j] = ex2(e[ts][nt][j]);
+      w.l[nt] += (e[ts][nt][0] + e[ts][nt][1]) + (e[ts][nt][2] + e[ts][nt][3]);
+    }
+#pragma unroll
+  for (int ts = 0; ts < TS; ++ts) v_product<C>(stage + C::OFF_VC, vsz, w, ts, e[ts]);
 }
 
 // ------------------------------------------------------------------ writing a unit or a piece
 __device__ __forceinline__ float lse_of(float m, float l) { return l > 0.0f ? (m + log2f(l)) * kLn2 : -INFINITY; }
 
-// A piece: (max, sum) of 8 NT rows, then their partial outputs.
+// A piece: (reference, sum) of 8 NT rows, then their partial outputs.
 template <int D, int NT>
 constexpr int piece_floats() { return 8 * NT * (D + 2); }
 
-template <int D, int NT, bool G32>
-__device__ __forceinline__ void flush(const MultiArgs& a, Work<D, NT, G32>& w, float* piece) {
-  using W = Work<D, NT, G32>;
+// Channel of output register (mt, half) for lane gid: runs of CH channels.
+template <typename C>
+__device__ __forceinline__ int out_channel(int mt, int half, int gid) {
+  return (mt / C::TPB) * 8 * C::CH + gid * C::CH + (mt % C::TPB) * 2 + half;
+}
+
+template <typename C>
+__device__ __forceinline__ void flush(const MultiArgs& a, Work<C>& w, float* piece) {
+  constexpr int NT = C::NT, NG = C::NG;
   const int lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
-  const bool wide = a.vb == 16;
   const int rows = min(8 * NT, w.n * a.r - w.rb * 8 * NT);
+  const float unit = w.top * (1.0f / (float)(1 << kTop));
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     float l = w.l[nt];
     l += __shfl_xor_sync(kFull, l, 1);
     l += __shfl_xor_sync(kFull, l, 2);
+    const float m = w.live[nt] ? w.ref[nt] : -INFINITY;
 #pragma unroll
-    for (int gi = 0; gi < W::NG; ++gi) {
+    for (int gi = 0; gi < NG; ++gi) {
       float z = w.zacc[nt][gi];
       z += __shfl_xor_sync(kFull, z, 1);
       z += __shfl_xor_sync(kFull, z, 2);
@@ -642,40 +824,32 @@ __device__ __forceinline__ void flush(const MultiArgs& a, Work<D, NT, G32>& w, f
     const int mine = nt * 8 + gid;
     if (tig == 0 && mine < rows) {
       if (piece != nullptr) {
-        *reinterpret_cast<float2*>(piece + 2 * mine) = make_float2(w.m[nt], l);
+        *reinterpret_cast<float2*>(piece + 2 * mine) = make_float2(m, l);
       } else if (a.lse != nullptr) {
-        const int row = w.rb * 8 * NT + mine;
-        a.lse[(long long)(w.c0 + row / a.r) * a.Hq + w.g * a.r + row % a.r] = lse_of(w.m[nt], l);
+        a.lse[w.orow[nt]] = lse_of(m, l);
       }
     }
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       const int src = 4 * (2 * tig + j), col = nt * 8 + 2 * tig + j;
       const float lc = __shfl_sync(kFull, l, src);
-      float z[W::NG];
+      const int orow = __shfl_sync(kFull, w.orow[nt], src);
+      float z[NG];
 #pragma unroll
-      for (int gi = 0; gi < W::NG; ++gi) z[gi] = __shfl_sync(kFull, w.zacc[nt][gi], src);
+      for (int gi = 0; gi < NG; ++gi) z[gi] = __shfl_sync(kFull, w.zacc[nt][gi], src);
       const float f = piece != nullptr ? 1.0f : (lc > 0.0f ? 1.0f / lc : 0.0f);
       if (col < rows) {
-        float* dst;
-        if (piece != nullptr) {
-          dst = piece + 16 * NT + col * D;
-        } else {
-          const int row = w.rb * 8 * NT + col;
-          dst = a.out + ((long long)(w.c0 + row / a.r) * a.Hq + w.g * a.r + row % a.r) * D;
-        }
+        float* dst = piece != nullptr ? piece + 16 * NT + col * C::D : a.out + (long long)orow * C::D;
 #pragma unroll
-        for (int mt = 0; mt < W::MT; mt += 2) {
-          // at G = 128 both 64-channel blocks share slot 0
-          const float zz = G32 ? z[mt / 2] : (D / a.G < W::NG ? z[0] : z[mt / 4]);
-          if (G32 && wide) {  // 16-bit runs span both 32-channel slots, which hold no zeros
-            *reinterpret_cast<float4*>(dst + out_channel<D, G32>(mt, 0, gid, true)) =
-                make_float4(w.o[mt][nt][j] * f, w.o[mt][nt][2 + j] * f, w.o[mt + 1][nt][j] * f, w.o[mt + 1][nt][2 + j] * f);
-          } else {
-            *reinterpret_cast<float4*>(dst + out_channel<D, G32>(mt, 0, gid, wide)) =
-                make_float4((w.o[mt][nt][j] + zz) * f, (w.o[mt][nt][2 + j] + zz) * f, (w.o[mt + 1][nt][j] + zz) * f,
-                            (w.o[mt + 1][nt][2 + j] + zz) * f);
+        for (int mt = 0; mt < C::MT; mt += 2) {
+          float y[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int c = ((mt + i / 2) % C::TPB) * 2 + (i & 1);  // the code's place in its run
+            const float x = w.o[mt + i / 2][nt][2 * (i & 1) + j] * (C::VB == 16 ? 1.0f : unit * (1.0f / (float)(1 << code_off<C::VB>(c))));
+            y[i] = (C::VB == 16 ? x : x + z[mt / C::TPB / C::GRUNS]) * f;
           }
+          *reinterpret_cast<float4*>(dst + out_channel<C>(mt, 0, gid)) = make_float4(y[0], y[1], y[2], y[3]);
         }
       }
     }
@@ -683,125 +857,200 @@ __device__ __forceinline__ void flush(const MultiArgs& a, Work<D, NT, G32>& w, f
 }
 
 // ------------------------------------------------------------------ the kernel
-// A cut unit: its tiles [u0, u1) in the list, and whose it is.
+// A cut unit: its tiles [u0, u1) in the list, the rows it stands for, the
+// runs that hold its pieces, and for one cut between CTAs the CTAs that do
+// (first piece in slot).
 struct Cut {
-  int u0, u1, b, ui;
+  int u0, u1, c0, g, row0, rows, k0, k1, ck0, ck1, slot;
 };
 
-// The tile that a warp looks at next.
-struct Cursor {
+// Where tile x of the list lies: sequence, unit of it, tile of that.
+struct Place {
   Seq s;
   int b, ui, ti;
 };
 
-template <int NT>
-__device__ __forceinline__ void seek(const MultiArgs& a, const int* first, int x, Cursor& c) {
+template <int NT, int TT>
+__device__ __forceinline__ Place seek(const MultiArgs& a, const int* first, int x) {
   int lo = 0, hi = a.B - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
     if (first[mid] <= x) lo = mid; else hi = mid - 1;
   }
-  c.b = lo;
-  c.s = load_seq<NT>(a, lo);
+  Place p;
+  p.b = lo;
+  p.s = load_seq<NT, TT>(a, lo);
   const int rem = x - first[lo];
-  c.ui = rem / c.s.cnt;
-  c.ti = rem % c.s.cnt;
+  p.ui = rem / p.s.cnt;
+  p.ti = rem - p.ui * p.s.cnt;
+  return p;
 }
 
-template <int NT>
-__device__ __forceinline__ void advance(const MultiArgs& a, const int* first, Cursor& c) {
-  if (++c.ti < c.s.cnt) return;
-  c.ti = 0;
-  if (++c.ui < c.s.units) return;
-  c.ui = 0;
-  do ++c.b; while (c.b < a.B && first[c.b + 1] == first[c.b]);  // past sequences without new tokens
-  if (c.b < a.B) c.s = load_seq<NT>(a, c.b);
+// The tile that a warp fetches next.
+struct Feed {
+  int b, ui, left;             // tiles left in the unit, this one among them
+  int t0, T, edge, to;         // its first token; behind the prefix tiles, at edge, comes to
+  int cnt, units, rbs, begin;  // rbs: row blocks of a KV head; begin: first token of a unit
+  long long base;              // contiguous: the head's first row; paged: the sequence's first table entry
+  bool fresh;                  // the warp's first tile of the unit
+};
+
+__device__ __forceinline__ void feed_base(const MultiArgs& a, Feed& f) {
+  f.base = a.table == nullptr ? ((long long)f.b * a.Hkv + f.ui / f.rbs) * a.T_cap : (long long)f.b * a.pps;
 }
 
-__device__ __forceinline__ int tile_pos(const Seq& s, int ti, int tt) { return (ti < s.np ? ti : s.t_lo + ti - s.np) * tt; }
+template <int NT, int TT>
+__device__ __forceinline__ void feed_from(const MultiArgs& a, const Place& p, Feed& f) {
+  f.b = p.b; f.ui = p.ui; f.left = p.s.cnt - p.ti;
+  f.T = p.s.T; f.edge = p.s.np * TT; f.to = p.s.t_lo * TT;
+  f.cnt = p.s.cnt; f.units = p.s.units; f.rbs = p.s.units / a.Hkv;
+  f.begin = p.s.np > 0 ? 0 : f.to;
+  f.t0 = p.ti < p.s.np ? p.ti * TT : f.to + (p.ti - p.s.np) * TT;
+  f.fresh = true;
+  feed_base(a, f);
+}
 
-// Start the copies of a tile into a stage; the bytes complete on bar.
-__device__ __forceinline__ void fetch_tile(const MultiArgs& a, const Cursor& c, int rbs, uint8_t* stage, uint64_t* bar,
-                                           int krb, int vrb, int ng, uint64_t policy) {
-  const int t0 = tile_pos(c.s, c.ti, a.tt);
-  int n = min(a.tt, c.s.T - t0);
-  if (n <= 0) return;
-  if (ng & 1) n += n & 1;  // (scale, zero) rows of 8 bytes go in pairs; the capacity is even then
-  const int g = c.ui / rbs;
-  long long row;
-  if (a.table == nullptr) {
-    row = ((long long)c.b * a.Hkv + g) * a.T_cap + t0;
+template <int NT, int TT>
+__device__ __forceinline__ void feed_next(const MultiArgs& a, const int* first, Feed& f) {
+  f.fresh = false;
+  if (--f.left > 0) {
+    f.t0 += TT;
+    if (f.t0 == f.edge) f.t0 = f.to;
+    return;
+  }
+  if (f.ui + 1 < f.units) {
+    ++f.ui;
+    f.left = f.cnt;
+    f.t0 = f.begin;
+    f.fresh = true;
+    feed_base(a, f);
   } else {
-    int page = __ldg(a.table + (long long)c.b * a.pps + t0 / kPageTokens);
-    if (page < 0 || page >= a.num_pages) {
-      atomicMax(a.status, kStatusInvalidArg);
-      page = 0;
+    int b = f.b;
+    do ++b; while (b < a.B && first[b + 1] == first[b]);  // past sequences without new tokens
+    if (b < a.B) feed_from<NT, TT>(a, Place{load_seq<NT, TT>(a, b), b, 0, 0}, f);
+  }
+}
+
+// What a stage holds: first token, staged tokens (0: nothing to see, no copy),
+// sequence and unit.
+constexpr int kFresh = 1 << 8, kEnd = 1 << 9;
+
+// Start the copies of a tile into a stage, one lane each; the bytes complete on bar.
+template <typename C>
+__device__ __forceinline__ void fetch_tile(const MultiArgs& a, const Feed& f, uint8_t* stage, int4* what, uint64_t* bar,
+                                           const uint8_t* src, int row_bytes, int off, uint64_t policy) {
+  const int lane = threadIdx.x & 31;
+  int n = max(0, min(C::TT, f.T - f.t0));
+  if (lane == 0) *what = make_int4(f.t0, n | (f.fresh ? kFresh : 0) | (f.left == 1 ? kEnd : 0), f.b, f.ui);
+  if (n > 0) {
+    // (scale, zero) rows of 8 bytes go in pairs; the capacity is even then
+    if constexpr ((C::NG & 1) && (C::KB < 16 || C::VB < 16)) n += n & 1;
+    long long row;
+    if (a.table == nullptr) {
+      row = f.base + f.t0;
+    } else {
+      int page = __ldg(a.table + f.base + f.t0 / kPageTokens);
+      if (page < 0 || page >= a.num_pages) {
+        if (lane == 0) atomicMax(a.status, kStatusInvalidArg);
+        page = 0;
+      }
+      row = ((long long)page * a.Hkv + f.ui / f.rbs) * kPageTokens + f.t0 % kPageTokens;
     }
-    row = ((long long)page * a.Hkv + g) * kPageTokens + t0 % kPageTokens;
+    constexpr int all = C::KRB + C::VRB + (C::KB < 16 ? C::NG * 8 : 0) + (C::VB < 16 ? C::NG * 8 : 0);
+    if (lane == 0) mbar_arrive_expect_tx(bar, n * all);
+    __syncwarp();
+    if (lane < 4 && row_bytes > 0) {
+      bulk_g2s(stage + off, src + row * row_bytes, n * row_bytes, bar, policy);
+    }
   }
-  const uint32_t kbytes = n * krb, vbytes = n * vrb, sz = n * ng * 8;
-  mbar_arrive_expect_tx(bar, kbytes + vbytes + (a.kb < 16 ? sz : 0) + (a.vb < 16 ? sz : 0));
-  bulk_g2s(stage, a.kc + row * krb, kbytes, bar, policy);
-  if (a.kb < 16) bulk_g2s(stage + a.off_ksz, a.ksz + row * ng * 2, sz, bar, policy);
-  bulk_g2s(stage + a.off_vc, a.vc + row * vrb, vbytes, bar, policy);
-  if (a.vb < 16) bulk_g2s(stage + a.off_vsz, a.vsz + row * ng * 2, sz, bar, policy);
 }
 
-// Join the pieces of a cut unit, one (row, 4 channels) element per thread and
-// step; piece k of [k0, k1) is at pieces + (2 k + slot) * PF, slot 1 when the
-// unit starts behind the k-th run's begin.  Writes the unit's output, or the
-// joined piece `to`.
-template <int D, int NT, typename Begin>
-__device__ __forceinline__ void join_element(const MultiArgs& a, const Cut& u, const Seq& s, int el, const float* pieces,
-                                             int k0, int k1, Begin begin, float* to) {
-  constexpr int PF = piece_floats<D, NT>();
-  const int row_in = el / (D / 4), d4 = el % (D / 4);
-  const int rbs = s.units / a.Hkv, g = u.ui / rbs, rb = u.ui % rbs;
-  const int row = rb * 8 * NT + row_in;
-  if (row >= s.n * a.r) return;
-  float M = -INFINITY, L = 0.0f;
+// Joining the pieces k0 .. k1 - 1 of a cut unit; at(k) is where piece k lies.
+// First the weights 2^(ref_k - max) of a row, then the sums of the outputs,
+// whose loads do not depend on one another.
+
+// Pieces of other CTAs are read past L1.
+template <bool L2, typename T>
+__device__ __forceinline__ T ld(const T* p) {
+  if constexpr (L2) return __ldcg(p);
+  else return *p;
+}
+
+// By one warp: the row's reference and sum, and its weights
+// (wt[(k - p0) * 8 NT + row]); a piece per lane and step.
+template <int NT, bool L2, typename At>
+__device__ __forceinline__ float2 join_row(int p0, int p1, const At& at, int row, float* wt) {
+  const int lane = threadIdx.x & 31;
+  float m = -INFINITY, l = 0.0f;
+  for (int k0 = p0; k0 < p1; k0 += 32) {
+    const int k = k0 + lane;
+    float2 ml = make_float2(-INFINITY, 0.0f);
+    if (k < p1) ml = ld<L2>(reinterpret_cast<const float2*>(at(k) + 2 * row));
+    float t = ml.x;
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) t = fmaxf(t, __shfl_xor_sync(kFull, t, off));
+    t = fmaxf(t, m);
+    if (k < p1) wt[(k - p0) * 8 * NT + row] = ml.x;  // its reference, until the largest is known
+    l *= m == t ? 1.0f : pow2i(m - t);                   // references are integers: exact
+    float part = ml.x == -INFINITY ? 0.0f : ml.y * pow2i(ml.x - t);
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) part += __shfl_xor_sync(kFull, part, off);
+    l += part;
+    m = t;
+  }
+  __syncwarp();
+  for (int k = p0 + lane; k < p1; k += 32) {
+    float& x = wt[(k - p0) * 8 * NT + row];
+    x = x == -INFINITY ? 0.0f : pow2i(x - m);
+  }
+  return make_float2(m, l);
+}
+
+// Four channels of the joined output: eight pieces in flight at a time.
+template <int NT, bool L2, typename At>
+__device__ __forceinline__ float4 join_out(int p0, int p1, const At& at, int row, int i, const float* wt) {
   float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-  for (int k = k0; k < k1; ++k) {
-    if (begin(k) == begin(k + 1)) continue;  // an empty run has no piece
-    const float* p = pieces + (long long)(2 * k + (u.u0 > begin(k) ? 1 : 0)) * PF;
-    const float2 ml = __ldcg(reinterpret_cast<const float2*>(p + 2 * row_in));
-    const float4 v = __ldcg(reinterpret_cast<const float4*>(p + 16 * NT + row_in * D) + d4);
-    const float m = fmaxf(M, ml.x);
-    if (m == -INFINITY) continue;
-    const float f = ex2(M - m), f2 = ex2(ml.x - m);
-    L = L * f + ml.y * f2;
-    o.x = o.x * f + v.x * f2; o.y = o.y * f + v.y * f2;
-    o.z = o.z * f + v.z * f2; o.w = o.w * f + v.w * f2;
-    M = m;
+  for (int k0 = p0; k0 < p1; k0 += 8) {
+    float4 v[8];
+    float f[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int k = k0 + j;
+      v[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      f[j] = 0.0f;
+      if (k < p1) {
+        v[j] = ld<L2>(reinterpret_cast<const float4*>(at(k) + 16 * NT) + i);
+        f[j] = wt[(k - p0) * 8 * NT + row];
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      o.x = fmaf(v[j].x, f[j], o.x); o.y = fmaf(v[j].y, f[j], o.y);
+      o.z = fmaf(v[j].z, f[j], o.z); o.w = fmaf(v[j].w, f[j], o.w);
+    }
   }
-  if (to != nullptr) {
-    if (d4 == 0) *reinterpret_cast<float2*>(to + 2 * row_in) = make_float2(M, L);
-    reinterpret_cast<float4*>(to + 16 * NT + row_in * D)[d4] = o;
-  } else {
-    const long long at = (long long)(s.c0 + row / a.r) * a.Hq + g * a.r + row % a.r;
-    const float f = L > 0.0f ? 1.0f / L : 0.0f;
-    reinterpret_cast<float4*>(a.out + at * D)[d4] = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
-    if (d4 == 0 && a.lse != nullptr) a.lse[at] = lse_of(M, L);
-  }
+  return o;
 }
 
-template <int D, int NT, bool G32>
-__global__ void __launch_bounds__(32 * kWarpsFor(NT), 1) multi_kernel(MultiArgs a) {
+template <typename C>
+__global__ void __launch_bounds__(32 * C::WARPS, 1) multi_kernel(MultiArgs a) {
   extern __shared__ __align__(128) uint8_t smem[];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, W = blockDim.x / 32;
+  constexpr int D = C::D, NT = C::NT, TT = C::TT, W = C::WARPS, ST = C::STAGES;
   constexpr int PF = piece_floats<D, NT>();
-  const int ng = D / a.G;
-  const int krb = D * a.kb / 8, vrb = D * a.vb / 8;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
 
   __shared__ int s_wsum[32];
-  __shared__ Cut s_cut[kMaxWarps + 1];
-  __shared__ int s_ncut;
+  __shared__ Cut s_cut[W + 1];
+  __shared__ int s_ncut, s_begin[W + 1];
   __shared__ int s_last[2];
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem);
-  float* tr = reinterpret_cast<float*>(smem + a.off_tr) + warp * 128 * NT;
-  int* first = reinterpret_cast<int*>(smem + a.off_first);
-  uint8_t* ring = smem + a.off_ring + (size_t)warp * a.stages * a.stage_bytes;
-  uint64_t* bar = bars + warp * a.stages;
+  __shared__ uint64_t s_bar[W * ST];
+  __shared__ int4 s_what[W * ST];
+  static_assert(Scratch<C>::kBytes <= C::SCRATCH, "a warp's scratch fits");
+  uint8_t* ring = smem + (size_t)warp * ST * C::STAGE;
+  float* tr = reinterpret_cast<float*>(smem + W * ST * C::STAGE + warp * C::SCRATCH);
+  int* first = reinterpret_cast<int*>(smem + W * (ST * C::STAGE + C::SCRATCH));
+  uint64_t* bar = s_bar + warp * ST;
+  int4* what = s_what + warp * ST;
 
   // tiles before each sequence
   {
@@ -809,7 +1058,7 @@ __global__ void __launch_bounds__(32 * kWarpsFor(NT), 1) multi_kernel(MultiArgs 
     const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
     int mine = 0;
     for (int b = b0; b < b1; ++b) {
-      const Seq s = load_seq<NT>(a, b);
+      const Seq s = load_seq<NT, TT>(a, b);
       mine += s.units * s.cnt;
       first[b] = s.units * s.cnt;
       if (blockIdx.x == 0) {
@@ -829,7 +1078,7 @@ __global__ void __launch_bounds__(32 * kWarpsFor(NT), 1) multi_kernel(MultiArgs 
       if (lane >= off) incl += y;
     }
     if (lane == 31) s_wsum[warp] = incl;
-    if (lane < a.stages) mbar_init(bar + lane, 1);
+    if (lane < ST) mbar_init(bar + lane, 1);
     fence_mbar_init();
     __syncthreads();
     int run = incl - mine;
@@ -841,139 +1090,181 @@ __global__ void __launch_bounds__(32 * kWarpsFor(NT), 1) multi_kernel(MultiArgs 
   const int total = first[a.B];
   if (total == 0) return;
   // as many CTAs as give every warp a tile: fewer cuts, and no join between CTAs for small calls
-  const int C = min((int)gridDim.x, (total + W - 1) / W);
+  const int ctas = min((int)gridDim.x, (total + W - 1) / W);
   const int cta = blockIdx.x;
-  if (cta >= C) return;
-  auto cta_begin = [&](int c) { return (int)((long long)total * c / C); };
+  if (cta >= ctas) return;
+  auto cta_begin = [&](int c) { return (int)((long long)total * c / ctas); };
   const int x0 = cta_begin(cta), x1 = cta_begin(cta + 1);
   auto warp_begin = [&](int w) { return x0 + (int)((long long)(x1 - x0) * w / W); };
 
+  float* const early = a.pieces + (long long)cta * W * PF;  // pieces of units that end inside a run, one per warp
+  static_assert(PF * 4 <= ST * C::STAGE, "a run's last piece fits its ring");
   {
     const int w0 = warp_begin(warp), w1 = warp_begin(warp + 1);
-    float* pieces = a.pieces + (long long)(cta * W + warp) * 2 * PF;
-    const uint64_t limit = *a.timeout_ns ? *a.timeout_ns : 2000000000ull;
-    const uint64_t policy = policy_evict_first();
-    bool dead = false;
     if (w0 < w1) {
-      Cursor c, f;  // the tile being used and the tile being fetched
-      seek<NT>(a, first, w0, c);
-      f = c;
+      const uint64_t limit = *a.timeout_ns ? *a.timeout_ns : 2000000000ull;
+      const uint64_t policy = policy_evict_first();
+      // lanes 0 .. 3 copy K codes, K pairs, V codes, V pairs
+      const uint8_t* src = lane == 0 ? a.kc : lane == 1 ? reinterpret_cast<const uint8_t*>(a.ksz)
+                           : lane == 2 ? a.vc : reinterpret_cast<const uint8_t*>(a.vsz);
+      const int row_bytes = lane == 0 ? C::KRB : lane == 1 ? (C::KB < 16 ? C::NG * 8 : 0)
+                            : lane == 2 ? C::VRB : (C::VB < 16 ? C::NG * 8 : 0);
+      const int off = lane == 0 ? 0 : lane == 1 ? C::OFF_KSZ : lane == 2 ? C::OFF_VC : C::OFF_VSZ;
+      const Place p = seek<NT, TT>(a, first, w0);
+      bool here = p.ti == 0;  // the unit at hand begins in this run
+      Feed f;
+      feed_from<NT, TT>(a, p, f);
       int fx = w0;
-      for (int i = 0; i < a.stages && fx < w1; ++i, ++fx) {
-        if (lane == 0) fetch_tile(a, f, f.s.units / a.Hkv, ring + i * a.stage_bytes, bar + i, krb, vrb, ng, policy);
-        advance<NT>(a, first, f);
+      for (int i = 0; i < ST && fx < w1; ++i, ++fx) {
+        if (i > 0) feed_next<NT, TT>(a, first, f);
+        fetch_tile<C>(a, f, ring + i * C::STAGE, what + i, bar + i, src, row_bytes, off, policy);
       }
-      Work<D, NT, G32> w;
-      load_unit<D, NT, G32>(a, c.s, c.b, c.ui, w);
+      __syncwarp();
+      Work<C> w;
+      bool dead = false;
       int st = 0;
       uint32_t parity = 0;  // bit i: phase of stage i
       for (int x = w0; x < w1; ++x) {
-        const int t0 = tile_pos(c.s, c.ti, a.tt);
-        const int n = min(a.tt, c.s.T - t0);
-        uint8_t* stage = ring + st * a.stage_bytes;
-        if (n > 0) {
+        const int4 d = what[st];
+        uint8_t* stage = ring + st * C::STAGE;
+        if (d.y & kFresh) {
+          load_unit<C>(a, load_seq<NT, TT>(a, d.z), d.z, d.w, w);
+          here = here || x > w0;
+        }
+        if (d.y & 0xFF) {
           if (!dead && !mbar_wait(bar + st, parity >> st & 1, limit)) {
             if (lane == 0) atomicMax(a.status, kStatusTimeout);
             dead = true;
           }
           dead = __any_sync(kFull, dead);
           parity ^= 1u << st;
-          if (!dead) {
-            const float* ksz = reinterpret_cast<const float*>(stage + a.off_ksz);
-            const float* vsz = reinterpret_cast<const float*>(stage + a.off_vsz);
-            for (int k = 0; k < n; k += 16)
-              step16<D, NT, G32>(a, w, stage + k * krb, ksz + k * ng * 2, stage + a.off_vc + k * vrb, vsz + k * ng * 2, tr,
-                                 t0 + k, ng);
-          }
+          if (!dead) tile_step<C>(a, w, stage, tr, d.x);
+          fence_proxy_async_smem();  // the stage's reads and writes come before the copies that refill it
         }
         __syncwarp();
-        if (fx < w1) {
-          if (lane == 0 && !dead) {
-            fence_proxy_async_smem();
-            fetch_tile(a, f, f.s.units / a.Hkv, stage, bar + st, krb, vrb, ng, policy);
-          }
-          advance<NT>(a, first, f);
+        if (fx < w1 && !dead) {
+          feed_next<NT, TT>(a, first, f);
+          fetch_tile<C>(a, f, stage, what + st, bar + st, src, row_bytes, off, policy);
           ++fx;
         }
-        st = st + 1 == a.stages ? 0 : st + 1;
-        const bool end = c.ti + 1 == c.s.cnt;
-        if (end || x + 1 == w1) {
-          const int u0 = x - c.ti;  // the unit's first tile
-          const bool all = end && u0 >= w0;
-          flush<D, NT, G32>(a, w, all ? nullptr : pieces + (u0 > w0 ? PF : 0));
+        st = st + 1 == ST ? 0 : st + 1;
+        if ((d.y & kEnd) || x + 1 == w1 || dead) {
+          float* to = (d.y & kEnd) && here ? nullptr : x + 1 == w1 || dead ? reinterpret_cast<float*>(ring) : early + warp * PF;
+          flush<C>(a, w, to);
         }
-        if (x + 1 < w1) {
-          advance<NT>(a, first, c);
-          if (end) load_unit<D, NT, G32>(a, c.s, c.b, c.ui, w);
-        }
+        if (dead) break;
+        __syncwarp();
       }
       // after a wait that gave up: let the copies still in flight land before the shared memory goes
       if (dead)
-        for (int i = 0; i < a.stages; ++i) mbar_wait(bar + i, parity >> i & 1, 1000000ull);
+        for (int i = 0; i < ST; ++i) mbar_wait(bar + i, parity >> i & 1, 1000000ull);
+    } else {
+      // a run without tiles (fewer tiles than warps) leaves an empty piece
+      float* piece = reinterpret_cast<float*>(ring);
+      for (int i = lane; i < PF; i += 32) piece[i] = i < 16 * NT && !(i & 1) ? -INFINITY : 0.0f;
     }
   }
   __syncthreads();
 
-  // ---- units cut by a run end: one thread per boundary finds its unit
+  // ---- units cut by a run end: one lane per boundary finds its unit
+  auto cta_of = [&](int x) { return (int)((((long long)x + 1) * ctas - 1) / total); };
+  if (tid <= W) s_begin[tid] = tid < W ? warp_begin(tid) : x1;
   if (warp == 0) {
-    Cut u{0, 0, 0, 0};
+    Cut u{};
     bool cut = false;
     if (lane <= W) {
       const int x = lane < W ? warp_begin(lane) : x1;
       if (x < total) {
-        Cursor c;
-        seek<NT>(a, first, x, c);
-        u.u0 = x - c.ti; u.u1 = u.u0 + c.s.cnt; u.b = c.b; u.ui = c.ui;
+        const Place p = seek<NT, TT>(a, first, x);
+        u.u0 = x - p.ti;
+        u.u1 = u.u0 + p.s.cnt;
+        const int rbs = p.s.units / a.Hkv;
+        u.g = p.ui / rbs;
+        u.row0 = (p.ui - u.g * rbs) * 8 * NT;
+        u.rows = min(8 * NT, p.s.n * a.r - u.row0);
+        u.c0 = p.s.c0;
         cut = u.u0 < x;
       }
     }
     // boundaries rise, so equal units stand side by side (among those that cut)
-    unsigned cuts = __ballot_sync(kFull, cut);
+    const unsigned cuts = __ballot_sync(kFull, cut);
     const unsigned below = cuts & ((1u << lane) - 1u);
     const int prev = below ? 31 - __clz(below) : 0;
     const int pu = __shfl_sync(kFull, u.u0, prev);
     const bool lead = cut && (!below || pu != u.u0);
     const unsigned leads = __ballot_sync(kFull, lead);
-    if (lead) s_cut[__popc(leads & ((1u << lane) - 1u))] = u;
+    if (lead) {
+      // its pieces: the runs that reach past its begin and start before its end
+      u.k0 = 0;
+      u.k1 = W;
+      while (warp_begin(u.k0 + 1) <= u.u0) ++u.k0;
+      while (warp_begin(u.k1 - 1) >= u.u1) --u.k1;
+      if (u.u0 < x0 || u.u1 > x1) {
+        u.ck0 = cta_of(u.u0);
+        u.ck1 = cta_of(u.u1 - 1) + 1;
+        u.slot = u.u0 > cta_begin(u.ck0) ? 1 : 0;
+      }
+      s_cut[__popc(leads & ((1u << lane) - 1u))] = u;
+    }
     if (lane == 0) { s_ncut = __popc(leads); s_last[0] = s_last[1] = 0; }
   }
   __syncthreads();
   const int ncut = s_ncut;
-  constexpr int EL = 8 * NT * D / 4;
-  const float* mine = a.pieces + (long long)cta * W * 2 * PF;
-  float* cpieces = a.cpieces;
-  bool shared_any = false;
-  for (int i = 0; i < ncut; ++i) {
-    const Cut u = s_cut[i];
-    const bool shared = u.u0 < x0 || u.u1 > x1;
-    shared_any |= shared;
+  if (ncut == 0) return;
+  constexpr int ROWS = 8 * NT, EL = ROWS * D / 4;
+  // in the scratch of the warps; the rings hold pieces
+  float2* s_ml = reinterpret_cast<float2*>(smem + W * ST * C::STAGE);  // [cuts][ROWS]
+  float* s_wt = reinterpret_cast<float*>(s_ml + (W + 1) * ROWS);       // [cut + piece][ROWS]
+  static_assert(((W + 1) * 2 + 2 * W + 1) * ROWS * 4 <= W * C::SCRATCH, "sums and weights fit the scratch");
+  auto is_shared = [&](const Cut& u) { return u.u0 < x0 || u.u1 > x1; };
+  auto out_row = [&](const Cut& u, int row) {
+    const int i = (u.row0 + row) / a.r;
+    return (long long)(u.c0 + i) * a.Hq + u.g * a.r + (u.row0 + row) - i * a.r;
+  };
+  auto write_row = [&](const Cut& u, int row, float2 ml) {
+    if (a.lse != nullptr) a.lse[out_row(u, row)] = lse_of(ml.x, ml.y);
+  };
+  auto write_out = [&](const Cut& u, int row, int d4, float2 ml, float4 o) {
+    const float f = ml.y > 0.0f ? 1.0f / ml.y : 0.0f;
+    reinterpret_cast<float4*>(a.out + out_row(u, row) * D)[d4] = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+  };
+  // a run's last piece lies in its ring, the piece of a unit that ends earlier in the workspace
+  auto piece_of = [&](const Cut& u, int k) -> const float* {
+    if (k == u.k1 - 1 && u.u1 < s_begin[k + 1]) return early + k * PF;
+    return reinterpret_cast<const float*>(smem + (size_t)k * ST * C::STAGE);
+  };
+  float* const to0 = a.cpieces + (long long)2 * cta * PF;
+  for (int i = warp; i < ncut * ROWS; i += W) {
+    const Cut& u = s_cut[i / ROWS];
+    const int row = i % ROWS;
+    if (row >= u.rows) continue;
+    const float2 ml = join_row<NT, false>(u.k0, u.k1, [&](int k) { return piece_of(u, k); }, row, s_wt + (u.k0 + i / ROWS) * ROWS);
+    if (lane != 0) continue;
+    s_ml[i] = ml;
+    if (is_shared(u)) *reinterpret_cast<float2*>(to0 + (u.u0 > x0 ? PF : 0) + 2 * row) = ml;
+    else write_row(u, row, ml);
   }
-  for (int el = tid; el < ncut * EL; el += blockDim.x) {
-    const Cut u = s_cut[el / EL];
-    const Seq s = load_seq<NT>(a, u.b);
-    const bool shared = u.u0 < x0 || u.u1 > x1;
-    int k0 = 0, k1 = W;
-    while (k0 < W && warp_begin(k0 + 1) <= u.u0) ++k0;
-    while (k1 > k0 && warp_begin(k1 - 1) >= u.u1) --k1;
-    float* to = shared ? cpieces + (long long)(2 * cta + (u.u0 > x0 ? 1 : 0)) * PF : nullptr;
-    join_element<D, NT>(a, u, s, el % EL, mine, k0, k1, warp_begin, to);
+  __syncthreads();
+  for (int el = tid; el < ncut * EL; el += 32 * W) {
+    const int i = el / EL, at = el % EL, row = at / (D / 4);
+    const Cut& u = s_cut[i];
+    if (row >= u.rows) continue;
+    const float4 o = join_out<NT, false>(u.k0, u.k1, [&](int k) { return piece_of(u, k); }, row, at, s_wt + (u.k0 + i) * ROWS);
+    if (is_shared(u)) reinterpret_cast<float4*>(to0 + (u.u0 > x0 ? PF : 0) + 16 * NT)[at] = o;
+    else write_out(u, row, at % (D / 4), s_ml[i * ROWS + row], o);
   }
-  if (!shared_any) return;
+  // a unit that began in an earlier CTA can only be the first, one that ends in a later the last
+  if (!is_shared(s_cut[0]) && !is_shared(s_cut[ncut - 1])) return;
 
   // ---- units cut between CTAs: the last to arrive joins the CTAs' pieces
-  __threadfence();
   __syncthreads();
-  auto cta_of = [&](int x) { return (int)((((long long)x + 1) * C - 1) / total); };
   if (tid < 2) {
     const int i = tid == 0 ? 0 : ncut - 1;
-    const Cut u = s_cut[i];
-    const bool shared = (u.u0 < x0 || u.u1 > x1) && (tid == 0 || i != 0);
-    if (shared) {
-      const int want = cta_of(u.u1 - 1) - cta_of(u.u0) + 1;
-      int* arrive = a.arrive + cta_of(u.u0);  // a CTA begins at most one unit that it does not end
+    const Cut& u = s_cut[i];
+    if (is_shared(u) && (tid == 0 || i != 0)) {
       __threadfence();
-      const int got = atomicAdd(arrive, 1) + 1;
-      if (got == want) {
+      int* arrive = a.arrive + u.ck0;  // a CTA begins at most one unit that it does not end
+      if (atomicAdd(arrive, 1) + 1 == u.ck1 - u.ck0) {
         *arrive = 0;  // ready for the next call
         __threadfence();
         s_last[tid] = 1;
@@ -981,12 +1272,21 @@ __global__ void __launch_bounds__(32 * kWarpsFor(NT), 1) multi_kernel(MultiArgs 
     }
   }
   __syncthreads();
+  s_wt = reinterpret_cast<float*>(smem);  // the rings are done with
   for (int t = 0; t < 2; ++t) {
-    if (!s_last[t]) continue;
-    const Cut u = s_cut[t == 0 ? 0 : ncut - 1];
-    const Seq s = load_seq<NT>(a, u.b);
-    for (int el = tid; el < EL; el += blockDim.x)
-      join_element<D, NT>(a, u, s, el, cpieces, cta_of(u.u0), cta_of(u.u1 - 1) + 1, cta_begin, nullptr);
+    if (!s_last[t]) continue;  // the same for every thread
+    const Cut& u = s_cut[t == 0 ? 0 : ncut - 1];
+    auto at = [&](int k) -> const float* { return a.cpieces + (long long)(2 * k + (k == u.ck0 ? u.slot : 0)) * PF; };
+    for (int row = warp; row < u.rows; row += W) {
+      const float2 ml = join_row<NT, true>(u.ck0, u.ck1, at, row, s_wt);
+      if (lane != 0) continue;
+      s_ml[row] = ml;
+      write_row(u, row, ml);
+    }
+    __syncthreads();
+    for (int i = tid; i < u.rows * (D / 4); i += 32 * W)
+      write_out(u, i / (D / 4), i % (D / 4), s_ml[i / (D / 4)], join_out<NT, true>(u.ck0, u.ck1, at, i / (D / 4), i, s_wt));
+    __syncthreads();
   }
 }
 

@@ -1,0 +1,8 @@
+// multi_k16.cu -- the multi-token decode over 16-bit K.
+#include "multi_launch.cuh"
+
+namespace lkv {
+namespace multi {
+cudaError_t launch_multi_k16(const MultiArgs& a, int D, const MultiPlan& p, cudaStream_t s) { return launch_k<16>(a, D, p, s); }
+}  // namespace multi
+}  // namespace lkv

@@ -1,0 +1,8 @@
+// multi_k8.cu -- the multi-token decode over 8-bit K.
+#include "multi_launch.cuh"
+
+namespace lkv {
+namespace multi {
+cudaError_t launch_multi_k8(const MultiArgs& a, int D, const MultiPlan& p, cudaStream_t s) { return launch_k<8>(a, D, p, s); }
+}  // namespace multi
+}  // namespace lkv
