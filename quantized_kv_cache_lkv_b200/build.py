@@ -1,9 +1,11 @@
-"""Build liblkv.so (the CUDA library behind include/lkv.h) in-tree for sm_100a.
+"""Build liblkv.so (the CUDA library behind include/lkv.h) in-tree for sm_100a,
+and the CPython module _native.so that calls it with torch tensors.
 
 Each .cu file under csrc/ is compiled to an object under _build/ (in
 parallel), then all are linked into quantized_kv_cache_lkv_b200/liblkv.so
 with the CUDA runtime linked statically.  nvcc cross-compiles, so this works
-on a machine without a GPU.
+on a machine without a GPU.  csrc/binding.cpp is compiled by g++ against the
+headers of Python and torch.
 """
 import concurrent.futures as cf
 import glob
@@ -11,12 +13,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "liblkv.so")
+NATIVE = os.path.join(PKG, "_native.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "--expt-relaxed-constexpr", "-Xcompiler", "-fPIC",
@@ -59,7 +63,30 @@ def _compile(src, verbose):
     return obj, p.stderr
 
 
+def build_native(force: bool = False) -> str:
+    """_native.so: the torch libraries it needs are already loaded when it is imported."""
+    src = os.path.join(CSRC, "binding.cpp")
+    newest = max(os.path.getmtime(f) for f in (src, os.path.join(ROOT, "include", "lkv.h"), os.path.abspath(__file__)))
+    if not force and os.path.exists(NATIVE) and os.path.getmtime(NATIVE) >= newest:
+        return NATIVE
+    import torch
+    at = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    inc = [os.path.join(at, "include"), os.path.join(at, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    tmp = NATIVE + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *("-I" + d for d in inc), src, "-o", tmp,
+           "-L" + os.path.join(at, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    p = subprocess.run(cmd, capture_output=True, text=True)
+    if p.returncode != 0:
+        raise RuntimeError(f"g++ failed for {src}:\n{p.stdout}\n{p.stderr}")
+    os.replace(tmp, NATIVE)
+    return NATIVE
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
+    build_native(force)
     srcs = _sources()
     newest = max(os.path.getmtime(f) for f in srcs + _headers() + [os.path.abspath(__file__)])
     if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= newest:

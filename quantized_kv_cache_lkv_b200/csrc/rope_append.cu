@@ -27,12 +27,22 @@ namespace lkv {
 namespace {
 
 constexpr int kWarps = 4;
+constexpr int kBlocksPerSm = 6;  // 80 registers; 5 blocks: 103 us instead of 93 for 16384 tokens of 32 / 8 heads
+constexpr int kRun = 4;          // query batches of a warp in large calls (2: 129 us, 8: 96 us)
 
 __device__ __forceinline__ uint4 ld8(const uint16_t* p) { return __ldg(reinterpret_cast<const uint4*>(p)); }
 
-__device__ __forceinline__ void widen8(const uint4& u, float* x) {
-  x[0] = bf16_lo(u.x); x[1] = bf16_hi(u.x); x[2] = bf16_lo(u.y); x[3] = bf16_hi(u.y);
-  x[4] = bf16_lo(u.z); x[5] = bf16_hi(u.z); x[6] = bf16_lo(u.w); x[7] = bf16_hi(u.w);
+// 8 adjacent channels for packed fp32 arithmetic: e holds the even ones (0, 2),
+// (4, 6), o the odd ones (1, 3), (5, 7) -- the low and high halves of two
+// words, so that sums of adjacent values and pairs are whole-register
+// operations.
+struct Eight {
+  float2 e[2], o[2];
+};
+
+__device__ __forceinline__ Eight widen8(const uint4& u) {
+  return {{make_float2(bf16_lo(u.x), bf16_lo(u.y)), make_float2(bf16_lo(u.z), bf16_lo(u.w))},
+          {make_float2(bf16_hi(u.x), bf16_hi(u.y)), make_float2(bf16_hi(u.z), bf16_hi(u.w))}};
 }
 
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
@@ -40,32 +50,91 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
-__device__ __forceinline__ uint4 narrow8(const float* x) {
-  return make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]), pack2(x[6], x[7]));
+__device__ __forceinline__ uint4 narrow8(const Eight& v) {
+  return make_uint4(pack2(v.e[0].x, v.o[0].x), pack2(v.e[0].y, v.o[0].y), pack2(v.e[1].x, v.o[1].x), pack2(v.e[1].y, v.o[1].y));
 }
 
-// 1 / sqrt(mean of squares + eps) of a row: the lane's 16 adjacent channels in
-// two words of 8, then the row's lanes.
+// Sum of squares of 8 channels, pairwise, adjacent values first.
+__device__ __forceinline__ float squares8(const Eight& v) {
+  const float2 a = exact_add2(exact_mul2(v.e[0], v.e[0]), exact_mul2(v.o[0], v.o[0]));
+  const float2 b = exact_add2(exact_mul2(v.e[1], v.e[1]), exact_mul2(v.o[1], v.o[1]));
+  return (a.x + a.y) + (b.x + b.y);
+}
+
+__device__ __forceinline__ float rstd_of(float ss, float inv_d, float eps) {
+  return __fdiv_rn(1.0f, __fsqrt_rn(ss * inv_d + eps));
+}
+
+// 1 / sqrt(mean of squares + eps) of a row: the lane's 16 adjacent channels,
+// then the row's lanes.
 template <int D>
-__device__ __forceinline__ float row_rstd(const uint4& u0, const uint4& u1, float eps, unsigned mask) {
-  float x[16];
-  widen8(u0, x);
-  widen8(u1, x + 8);
-#pragma unroll
-  for (int i = 0; i < 16; ++i) x[i] = x[i] * x[i];
-#pragma unroll
-  for (int n = 8; n >= 1; n >>= 1)
-#pragma unroll
-    for (int i = 0; i < n; ++i) x[i] = x[2 * i] + x[2 * i + 1];
-  float t = x[0];
+__device__ __forceinline__ float row_rstd(const Eight& v0, const Eight& v1, float eps, unsigned mask) {
+  float t = squares8(v0) + squares8(v1);
 #pragma unroll
   for (int off = 1; off < D / 16; off <<= 1) t = t + __shfl_xor_sync(mask, t, off);
-  return __fdiv_rn(1.0f, __fsqrt_rn(t * (1.0f / D) + eps));
+  return rstd_of(t, 1.0f / D, eps);
 }
 
-__device__ __forceinline__ void norm8(float* x, float r, const float* w) {
+// The same when lane j holds the 8 channels from 8 j and the 8 from D/2 + 8 j.
+template <int D>
+__device__ __forceinline__ float row_rstd_halves(const Eight& v0, const Eight& v1, float eps, unsigned mask) {
+  float2 t = make_float2(squares8(v0), squares8(v1));
 #pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = (x[i] * r) * w[i];
+  for (int off = 1; off < D / 16; off <<= 1)
+    t = exact_add2(t, make_float2(__shfl_xor_sync(mask, t.x, off), __shfl_xor_sync(mask, t.y, off)));
+  return rstd_of(t.x + t.y, 1.0f / D, eps);
+}
+
+__device__ __forceinline__ void norm8(Eight& v, float r, const Eight& w) {
+  const float2 rr = f2(r);
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    v.e[i] = exact_mul2(exact_mul2(v.e[i], rr), w.e[i]);
+    v.o[i] = exact_mul2(exact_mul2(v.o[i], rr), w.o[i]);
+  }
+}
+
+// p + q for two rounded products.  A packed multiply that feeds a packed add
+// would be contracted by the code generator, so the sum is p * 1 + q with a 1
+// it does not know.
+__device__ __forceinline__ float2 sum_of_products(float2 p, float2 q, float one) { return exact_fma2(p, f2(one), q); }
+
+// (a, b) -> (a c - b s, b c + a s), with ns = -s.
+__device__ __forceinline__ void turn2(float2& a, float2& b, float2 c, float2 s, float2 ns, float one) {
+  const float2 x = sum_of_products(exact_mul2(a, c), exact_mul2(b, ns), one);
+  const float2 y = sum_of_products(exact_mul2(b, c), exact_mul2(a, s), one);
+  a = x;
+  b = y;
+}
+
+// (cos, sin) of 8 pairs, for channels in the order of Eight.
+struct Turns {
+  Eight c, s;
+};
+
+__device__ __forceinline__ Turns load_turns(const float* table) {  // 8 pairs (cos, sin) side by side
+  const float4* p = reinterpret_cast<const float4*>(table);
+  const float4 a = __ldg(p), b = __ldg(p + 1), c = __ldg(p + 2), d = __ldg(p + 3);
+  return {{{make_float2(a.x, b.x), make_float2(c.x, d.x)}, {make_float2(a.z, b.z), make_float2(c.z, d.z)}},
+          {{make_float2(a.y, b.y), make_float2(c.y, d.y)}, {make_float2(a.w, b.w), make_float2(c.w, d.w)}}};
+}
+
+__device__ __forceinline__ float2 neg2(float2 a) { return make_float2(-a.x, -a.y); }
+
+// Pairs (x_i, y_i), i = 0 .. 7.
+__device__ __forceinline__ void turn_halves(Eight& x, Eight& y, const Turns& t, float one) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    turn2(x.e[i], y.e[i], t.c.e[i], t.s.e[i], neg2(t.s.e[i]), one);
+    turn2(x.o[i], y.o[i], t.c.o[i], t.s.o[i], neg2(t.s.o[i]), one);
+  }
+}
+
+// Adjacent pairs inside 8 channels; cs: (cos, sin) of the 4 pairs.
+__device__ __forceinline__ void turn_adjacent(Eight& v, const float4& p, const float4& q, float one) {
+  const float2 c0 = make_float2(p.x, p.z), s0 = make_float2(p.y, p.w), c1 = make_float2(q.x, q.z), s1 = make_float2(q.y, q.w);
+  turn2(v.e[0], v.o[0], c0, s0, neg2(s0), one);
+  turn2(v.e[1], v.o[1], c1, s1, neg2(s1), one);
 }
 
 // Where a lane's two runs of 8 channels lie in a query row.
@@ -120,28 +189,19 @@ __device__ __forceinline__ long long slot_row(const RopeAppendArgs& a, long long
   return (page * a.Hkv + g) * a.page_tokens + slot % a.page_tokens;
 }
 
-// Query heads [h0, h1) of token t.
-template <int D, bool INTER>
-__device__ void query_rows(const RopeAppendArgs& a, int t, int pos, int h0, int h1) {
+// Query heads [h0, h1) of token t.  WHOLE: half layout with every channel
+// turning, where the sum of squares needs no other channels than the lane's.
+template <int D, bool INTER, bool WHOLE>
+__device__ __forceinline__ void query_rows(const RopeAppendArgs& a, int t, int pos, int h0, int h1) {
   constexpr int LPR = D / kDimsPerLane, RPW = 32 / LPR;
   const int lane = threadIdx.x & 31, j = lane % LPR, sub = lane / LPR;
   const unsigned mask = row_lane_mask<LPR>(lane);
-  const Runs run = query_runs<INTER>(j, a.rot);
+  const Runs run = WHOLE ? Runs{8 * j, D / 2 + 8 * j, true} : query_runs<INTER>(j, a.rot);
   const bool norm = a.q_weight != nullptr;
-  float wa[8], wb[8], cs[16];
-  if (norm) { widen8(ld8(a.q_weight + run.a), wa); widen8(ld8(a.q_weight + run.b), wb); }
-  if (run.turn) {  // 8 pairs from 8 j: (cos, sin) side by side
-    const float4* src = reinterpret_cast<const float4*>(a.table + ((long long)pos * (a.rot / 2) + 8 * j) * 2);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float4 v = __ldg(src + i);
-      cs[4 * i] = v.x; cs[4 * i + 1] = v.y; cs[4 * i + 2] = v.z; cs[4 * i + 3] = v.w;
-    }
-  }
+  const bool square = norm && !INTER && !WHOLE;  // the sum wants adjacent channels, the pairs others
   const uint16_t* src = a.q + t * a.q_stride;
   uint16_t* dst = a.q_out + (long long)t * a.Hq * D;
-  const bool square = norm && !INTER;  // the sum wants adjacent channels, the pairs others
-  uint4 ua, ub, s0, s1;
+  uint4 ua = make_uint4(0, 0, 0, 0), ub = ua, s0 = ua, s1 = ua;
   auto fetch = [&](int h) {
     if (h >= h1) return;
     const uint16_t* row = src + (long long)h * D;
@@ -150,36 +210,36 @@ __device__ void query_rows(const RopeAppendArgs& a, int t, int pos, int h0, int 
     if (square) { s0 = ld8(row + 16 * j); s1 = ld8(row + 16 * j + 8); }
   };
   fetch(h0 + sub);
+  Eight wa, wb;
+  if (norm) { wa = widen8(ld8(a.q_weight + run.a)); wb = widen8(ld8(a.q_weight + run.b)); }
+  Turns cs;
+  float4 near[4];
+  if (run.turn) {  // 8 pairs from 8 j
+    const float* at = a.table + ((long long)pos * (WHOLE ? D / 2 : a.rot / 2) + 8 * j) * 2;
+    if constexpr (INTER) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) near[i] = __ldg(reinterpret_cast<const float4*>(at) + i);
+    } else {
+      cs = load_turns(at);
+    }
+  }
   for (int h = h0 + sub; h - sub < h1; h += RPW) {
-    const uint4 va = ua, vb = ub, q0 = square ? s0 : ua, q1 = square ? s1 : ub;
+    Eight x = widen8(ua), y = widen8(ub);
+    const uint4 q0 = s0, q1 = s1;
     fetch(h + RPW);
     if (h >= h1) continue;  // the lanes of a row agree
-    float x[8], y[8];
-    widen8(va, x);
-    widen8(vb, y);
     if (norm) {
-      const float r = row_rstd<D>(q0, q1, a.eps, mask);
+      const float r = WHOLE ? row_rstd_halves<D>(x, y, a.eps, mask)
+                            : square ? row_rstd<D>(widen8(q0), widen8(q1), a.eps, mask) : row_rstd<D>(x, y, a.eps, mask);
       norm8(x, r, wa);
       norm8(y, r, wb);
     }
     if (run.turn) {
       if constexpr (INTER) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float p = x[2 * i], q = x[2 * i + 1], c = cs[2 * i], s = cs[2 * i + 1];
-          x[2 * i] = p * c - q * s;
-          x[2 * i + 1] = q * c + p * s;
-          const float p2 = y[2 * i], q2 = y[2 * i + 1], c2 = cs[8 + 2 * i], s2 = cs[8 + 2 * i + 1];
-          y[2 * i] = p2 * c2 - q2 * s2;
-          y[2 * i + 1] = q2 * c2 + p2 * s2;
-        }
+        turn_adjacent(x, near[0], near[1], a.one);
+        turn_adjacent(y, near[2], near[3], a.one);
       } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float p = x[i], q = y[i], c = cs[2 * i], s = cs[2 * i + 1];
-          x[i] = p * c - q * s;
-          y[i] = q * c + p * s;
-        }
+        turn_halves(x, y, cs, a.one);
       }
     }
     *reinterpret_cast<uint4*>(dst + (long long)h * D + run.a) = narrow8(x);
@@ -187,128 +247,135 @@ __device__ void query_rows(const RopeAppendArgs& a, int t, int pos, int h0, int 
   }
 }
 
-// Key heads g0 .. of token t, one batch of 32 / (D / 16) rows.
+// Key and value heads g0 .. of token t, one batch of 32 / (D / 16) rows.
+// All loads of the rows come before the first use, the slot's among them.
 template <int D, bool INTER>
-__device__ void key_rows(const RopeAppendArgs& a, int t, int pos, long long slot, int g0) {
+__device__ __forceinline__ void key_value_rows(const RopeAppendArgs& a, int t, int pos, int g0, bool keys, bool values) {
   constexpr int LPR = D / kDimsPerLane;
   const int lane = threadIdx.x & 31, j = lane % LPR, g = g0 + lane / LPR;
   const unsigned mask = row_lane_mask<LPR>(lane);
   if (g >= a.Hkv) return;
-  const long long row = slot_row(a, slot, g);
-  if (row < 0) return;
   const uint16_t* src = a.k + t * a.k_stride + (long long)g * D;
-  const uint4 u0 = ld8(src + 16 * j), u1 = ld8(src + 16 * j + 8);
-  float x[16];
-  widen8(u0, x);
-  widen8(u1, x + 8);
+  const uint16_t* vsrc = a.v + t * a.v_stride + (long long)g * D + 16 * j;
+  const int half = a.rot / 2;
+  const uint4 k0 = ld8(src + 16 * j), k1 = ld8(src + 16 * j + 8);
+  uint4 other[2] = {k0, k1};  // the partners of the lane's runs of 8 channels (half layout)
+  if constexpr (!INTER) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int c0 = 16 * j + 8 * e;
+      if (c0 < a.rot) other[e] = ld8(src + (c0 < half ? c0 + half : c0 - half));
+    }
+  }
+  uint4 v0 = k0, v1 = k1;
+  if (values) { v0 = ld8(vsrc); v1 = ld8(vsrc + 8); }
+  const long long row = slot_row(a, __ldg(reinterpret_cast<const long long*>(a.slots) + t), g);
+  if (values && row >= 0) {
+    const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+    store_row<D>(a, a.vb, w, a.v_codes, a.v_sz, row, j, mask);
+  }
+  if (!keys) return;
+  Eight x[2] = {widen8(k0), widen8(k1)};
   float r = 1.0f;
   if (a.k_weight != nullptr) {
-    r = row_rstd<D>(u0, u1, a.eps, mask);
-    float w[8];
-    widen8(ld8(a.k_weight + 16 * j), w);
-    norm8(x, r, w);
-    widen8(ld8(a.k_weight + 16 * j + 8), w);
-    norm8(x + 8, r, w);
+    r = row_rstd<D>(x[0], x[1], a.eps, mask);
+    norm8(x[0], r, widen8(ld8(a.k_weight + 16 * j)));
+    norm8(x[1], r, widen8(ld8(a.k_weight + 16 * j + 8)));
   }
 #pragma unroll
-  for (int e = 0; e < 2; ++e) {  // runs of 8 channels
+  for (int e = 0; e < 2; ++e) {
     const int c0 = 16 * j + 8 * e;
-    float* z = x + 8 * e;
     if (c0 >= a.rot) continue;
     if constexpr (INTER) {
-      const float4* src4 = reinterpret_cast<const float4*>(a.table + (long long)pos * a.rot + c0);
+      const float4* p = reinterpret_cast<const float4*>(a.table + (long long)pos * a.rot + c0);
+      turn_adjacent(x[e], __ldg(p), __ldg(p + 1), a.one);
+    } else {
+      const bool low = c0 < half;
+      Eight o = widen8(other[e]);
+      if (a.k_weight != nullptr) norm8(o, r, widen8(ld8(a.k_weight + (low ? c0 + half : c0 - half))));
+      const Turns cs = load_turns(a.table + ((long long)pos * half + (low ? c0 : c0 - half)) * 2);
+      // the first of a pair: a c + b (-s); the second: b c + a s
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const float4 v = __ldg(src4 + i);
-        const float p = z[4 * i], q = z[4 * i + 1], p2 = z[4 * i + 2], q2 = z[4 * i + 3];
-        z[4 * i] = p * v.x - q * v.y;
-        z[4 * i + 1] = q * v.x + p * v.y;
-        z[4 * i + 2] = p2 * v.z - q2 * v.w;
-        z[4 * i + 3] = q2 * v.z + p2 * v.w;
-      }
-    } else {
-      const int half = a.rot / 2;
-      const bool low = c0 < half;
-      const int other = low ? c0 + half : c0 - half, pair = low ? c0 : c0 - half;
-      float o[8];
-      widen8(ld8(src + other), o);
-      if (a.k_weight != nullptr) {
-        float w[8];
-        widen8(ld8(a.k_weight + other), w);
-        norm8(o, r, w);
-      }
-      const float4* src4 = reinterpret_cast<const float4*>(a.table + ((long long)pos * half + pair) * 2);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float4 v = __ldg(src4 + i);
-        const float p = z[2 * i], q = z[2 * i + 1], po = o[2 * i], qo = o[2 * i + 1];
-        // the first of a pair: a c - b s; the second: b c + a s
-        z[2 * i] = low ? p * v.x - po * v.y : p * v.x + po * v.y;
-        z[2 * i + 1] = low ? q * v.z - qo * v.w : q * v.z + qo * v.w;
+        x[e].e[i] = sum_of_products(exact_mul2(x[e].e[i], cs.c.e[i]), exact_mul2(o.e[i], low ? neg2(cs.s.e[i]) : cs.s.e[i]), a.one);
+        x[e].o[i] = sum_of_products(exact_mul2(x[e].o[i], cs.c.o[i]), exact_mul2(o.o[i], low ? neg2(cs.s.o[i]) : cs.s.o[i]), a.one);
       }
     }
   }
-  const uint4 n0 = narrow8(x), n1 = narrow8(x + 8);
+  if (row < 0) return;  // the lanes of a row agree
+  const uint4 n0 = narrow8(x[0]), n1 = narrow8(x[1]);
   const uint32_t w[8] = {n0.x, n0.y, n0.z, n0.w, n1.x, n1.y, n1.z, n1.w};
   store_row<D>(a, a.kb, w, a.k_codes, a.k_sz, row, j, mask);
 }
 
-template <int D>
-__device__ void value_rows(const RopeAppendArgs& a, int t, long long slot, int g0) {
-  constexpr int LPR = D / kDimsPerLane;
-  const int lane = threadIdx.x & 31, j = lane % LPR, g = g0 + lane / LPR;
-  const unsigned mask = row_lane_mask<LPR>(lane);
-  if (g >= a.Hkv) return;
-  const long long row = slot_row(a, slot, g);
-  if (row < 0) return;
-  const uint16_t* src = a.v + t * a.v_stride + (long long)g * D;
-  const uint4 u0 = ld8(src + 16 * j), u1 = ld8(src + 16 * j + 8);
-  const uint32_t w[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
-  store_row<D>(a, a.vb, w, a.v_codes, a.v_sz, row, j, mask);
+// The 128-byte lines of `bytes` bytes from p, one per lane, on their way into L2.
+__device__ __forceinline__ void prefetch_lines(const void* p, int bytes, int lane) {
+  if (lane >= 0 && lane * 128 < bytes) prefetch_l2(static_cast<const char*>(p) + lane * 128);
 }
 
-// One warp: one token and one of its items -- query runs, then key batches,
-// then value batches.
-template <int D, bool INTER>
-__global__ void __launch_bounds__(32 * kWarps) rope_append_kernel(RopeAppendArgs a, int q_items, int kv_items) {
+// One warp: one token and one of its items -- query runs, then key and value
+// batches.
+template <int D, bool INTER, bool WHOLE>
+__global__ void __launch_bounds__(32 * kWarps, kBlocksPerSm) rope_append_kernel(RopeAppendArgs a, int q_items, int kv_items) {
   constexpr int RPW = 32 / (D / kDimsPerLane);
-  const int items = q_items + 2 * kv_items;
+  const int items = q_items + kv_items;
   const long long id = (long long)blockIdx.x * kWarps + threadIdx.x / 32;
   const long long t = id / items;
   const int item = (int)(id % items);
   if (t >= a.n_cap) return;
+  const int lane = threadIdx.x & 31;
+  const bool query = item < q_items;
+  const int h0 = item * RPW * a.iters, h1 = min(a.Hq, h0 + RPW * a.iters);
+  const int kv = a.split ? (item - q_items) / 2 : item - q_items, g0 = kv * RPW, g1 = min(a.Hkv, g0 + RPW);
+  if (a.ahead > 0 && t + a.ahead < a.n_cap) {
+    // the same item of a token that no resident warp has reached yet
+    const long long u = t + a.ahead;
+    if (query) {
+      prefetch_lines(a.q + u * a.q_stride + h0 * D, (h1 - h0) * D * 2, lane);
+    } else {
+      prefetch_lines(a.k + u * a.k_stride + g0 * D, (g1 - g0) * D * 2, lane < 16 ? lane : -1);
+      prefetch_lines(a.v + u * a.v_stride + g0 * D, (g1 - g0) * D * 2, lane - 16);
+    }
+  }
   const int n = a.n_tokens ? clamp_len(__ldg(a.n_tokens), a.n_cap) : a.n_cap;
   const int pos = a.rot > 0 ? __ldg(a.positions + t) : 0;
   if (t >= n) return;
   if (a.rot > 0 && (pos < 0 || pos >= a.table_rows)) return;  // no such angle: the token is left out
-  if (item < q_items) {
-    const int h0 = item * RPW * a.iters;
-    query_rows<D, INTER>(a, (int)t, pos, h0, min(a.Hq, h0 + RPW * a.iters));
+  if (query) {
+    query_rows<D, INTER, WHOLE>(a, (int)t, pos, h0, h1);
   } else {
-    const long long slot = __ldg(reinterpret_cast<const long long*>(a.slots) + t);
-    if (item < q_items + kv_items) key_rows<D, INTER>(a, (int)t, pos, slot, (item - q_items) * RPW);
-    else value_rows<D>(a, (int)t, slot, (item - q_items - kv_items) * RPW);
+    const bool second = a.split && ((item - q_items) & 1);
+    key_value_rows<D, INTER>(a, (int)t, pos, g0, !second, !a.split || second);
   }
 }
 
-template <int D, bool INTER>
+template <int D, bool INTER, bool WHOLE>
 cudaError_t launch_t(RopeAppendArgs a, cudaStream_t s) {
   constexpr int RPW = 32 / (D / kDimsPerLane);
-  // one batch of rows a warp while that leaves SMs idle, else runs of four
+  // one batch of rows a warp while that leaves SMs idle, else runs of four and keys with values
   const long long batches = (long long)a.n_cap * ((a.Hq + RPW - 1) / RPW);
-  a.iters = batches >= (long long)num_sms() * 64 ? 4 : 1;
-  const int q_items = (a.Hq + RPW * a.iters - 1) / (RPW * a.iters), kv_items = (a.Hkv + RPW - 1) / RPW;
-  const long long blocks = ((long long)a.n_cap * (q_items + 2 * kv_items) + kWarps - 1) / kWarps;
+  const bool many = batches >= (long long)num_sms() * 64;
+  a.iters = many ? kRun : 1;
+  a.split = !many;
+  const int q_items = (a.Hq + RPW * a.iters - 1) / (RPW * a.iters), kv_items = (a.Hkv + RPW - 1) / RPW * (many ? 1 : 2);
+  // tokens that the resident warps hold at a time
+  a.ahead = many ? (int)((long long)num_sms() * kBlocksPerSm * kWarps / (q_items + kv_items)) + 1 : 0;
+  const long long blocks = ((long long)a.n_cap * (q_items + kv_items) + kWarps - 1) / kWarps;
   if (blocks >= (1ll << 31)) return cudaErrorInvalidValue;
-  rope_append_kernel<D, INTER><<<(unsigned)blocks, 32 * kWarps, 0, s>>>(a, q_items, kv_items);
+  rope_append_kernel<D, INTER, WHOLE><<<(unsigned)blocks, 32 * kWarps, 0, s>>>(a, q_items, kv_items);
   return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_rope_append(const RopeAppendArgs& a, int D, bool interleaved, cudaStream_t s) {
-  if (D == 64) return interleaved ? launch_t<64, true>(a, s) : launch_t<64, false>(a, s);
-  return interleaved ? launch_t<128, true>(a, s) : launch_t<128, false>(a, s);
+  const bool whole = !interleaved && a.rot == D;
+  if (D == 64) {
+    if (interleaved) return launch_t<64, true, false>(a, s);
+    return whole ? launch_t<64, false, true>(a, s) : launch_t<64, false, false>(a, s);
+  }
+  if (interleaved) return launch_t<128, true, false>(a, s);
+  return whole ? launch_t<128, false, true>(a, s) : launch_t<128, false, false>(a, s);
 }
 
 }  // namespace lkv

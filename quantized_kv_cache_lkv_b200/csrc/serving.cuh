@@ -37,6 +37,8 @@ struct RopeAppendArgs {
   uint8_t *k_codes, *v_codes;
   float *k_sz, *v_sz;
   int iters;                               // row batches of one warp's item
+  bool split;                              // keys and values as items of their own
+  int ahead;                               // tokens from an item to the one it prefetches (0: none)
 };
 
 cudaError_t launch_page_plan(const PlanArgs& a, cudaStream_t s);

@@ -56,8 +56,7 @@ class lkv_score_rule(ctypes.Structure):
                 ("slopes", ctypes.c_void_p), ("prefix_lens", ctypes.c_void_p), ("doc_starts", ctypes.c_void_p)]
 
     def __init__(self, softmax_scale, softcap=0.0, window=0, slopes=None, prefix_lens=None, doc_starts=None):
-        self.tensors = {"slopes": (slopes, "float32"), "prefix_lens": (prefix_lens, "int32"),
-                        "doc_starts": (doc_starts, "int32")}
+        self.tensors = (slopes, prefix_lens, doc_starts)
         super().__init__(softmax_scale, softcap, window, _ptr(slopes), _ptr(prefix_lens), _ptr(doc_starts))
 
 
@@ -147,11 +146,17 @@ def _check(rc, what):
         raise LkvError(rc, what)
 
 
+_specs = {}  # (k_bits, v_bits, group) -> lkv_qspec
+
+
 def _spec(spec):
     if isinstance(spec, lkv_qspec):
         return spec
     kb, vb, g = spec
-    return lkv_qspec(kb, vb, g)
+    got = _specs.get((kb, vb, g))
+    if got is None:
+        got = _specs[kb, vb, g] = lkv_qspec(kb, vb, g)
+    return got
 
 
 def _seg(seg):
@@ -302,58 +307,45 @@ def lkv_tiered_decode(B, Hq, Hkv, T_cap, D, group, seq_lens, mass, tau_low, tau_
 
 
 # ---------------------------------------------------------------- the serving step
-# The calls below check torch tensors before their addresses are passed on:
-# type, contiguity, room and device (integer addresses go through unchecked).
+# These calls go through the native module (csrc/binding.cpp), which checks torch
+# tensors -- type, contiguity, room and device -- before their addresses are
+# passed on, at a tenth of what the same checks cost here.  Integer addresses go
+# through unchecked.
+
+_nat = None
 
 
-def _want(what, x, dtype, numel, contiguous=True):
-    """Address of a torch tensor that has this type and at least this many values on the current device."""
-    if x is None or isinstance(x, int):
-        return x
-    import torch
-    if (x.dtype is not getattr(torch, dtype) or x.numel() < numel or (contiguous and not x.is_contiguous()) or
-            not x.is_cuda or x.device.index != torch.cuda.current_device()):
-        raise LkvError(LKV_ERR_INVALID_ARG, f"{what}: a tensor of {numel} or more contiguous {dtype} on the current device "
-                                            f"is wanted, not {tuple(x.shape)} {x.dtype} on {x.device}")
-    return x.data_ptr()
-
-
-def _want_cache(what, spec, rows, D, k_codes, k_sz, v_codes, v_sz):
-    """Addresses of the four cache tensors of `rows` rows."""
-    ng = D // spec.group if spec.group > 0 else 0
-    return (_want(what, k_codes, "uint8", rows * D * spec.k_bits // 8),
-            _want(what, k_sz, "float32", rows * ng * 2) if spec.k_bits != 16 else None,
-            _want(what, v_codes, "uint8", rows * D * spec.v_bits // 8),
-            _want(what, v_sz, "float32", rows * ng * 2) if spec.v_bits != 16 else None)
+def native():
+    """The native module, connected to liblkv.so (raises if either has not been built)."""
+    global _nat
+    if _nat is None:
+        import torch  # noqa: F401  (its libraries come before the module's)
+        try:
+            from . import _native
+        except ImportError as e:
+            raise RuntimeError("the _native module is missing: build it with "
+                               "`python -m quantized_kv_cache_lkv_b200.build`") from e
+        L = lib()
+        _native.connect(LkvError, *(ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in (
+            "lkv_page_plan", "lkv_rope_table", "lkv_rope_append_kv", "lkv_decode_attention_multi",
+            "lkv_decode_attention_multi_paged")))
+        _nat = _native
+    return _nat
 
 
 def lkv_page_plan(B, pages_per_seq, num_pages, n_cap, seq_lens, n_new, free_pages, free_cap, free_count, block_table,
                   new_lens, cu_new, positions, token_seq, slots, free_left, status, stream=None):
-    w = "lkv_page_plan"
-    _check(lib().lkv_page_plan(B, pages_per_seq, num_pages, n_cap, _want(w, seq_lens, "int32", B),
-                               _want(w, n_new, "int32", B), _want(w, free_pages, "int32", free_cap), free_cap,
-                               _want(w, free_count, "int32", 1), _want(w, block_table, "int32", B * pages_per_seq),
-                               _want(w, new_lens, "int32", B), _want(w, cu_new, "int32", B + 1),
-                               _want(w, positions, "int32", n_cap), _want(w, token_seq, "int32", n_cap),
-                               _want(w, slots, "int64", n_cap), _want(w, free_left, "int32", 1),
-                               _want(w, status, "int32", 1), _stream(stream)), w)
+    rc = (_nat or native()).lkv_page_plan(B, pages_per_seq, num_pages, n_cap, seq_lens, n_new, free_pages, free_cap,
+                                          free_count, block_table, new_lens, cu_new, positions, token_seq, slots,
+                                          free_left, status, stream)
+    if rc:
+        raise LkvError(rc, "lkv_page_plan")
 
 
 def lkv_rope_table(spec, rows, table, stream=None):
-    _check(lib().lkv_rope_table(spec, rows, _want("lkv_rope_table", table, "float32", rows * spec.rot_dim),
-                                _stream(stream)), "lkv_rope_table")
-
-
-def _token_rows(what, x, n, heads, D, stride):
-    """(address, elements from token to token) of [n][heads][D] rows: a view of a fused projection, or an
-    address with its stride."""
-    if x is None or isinstance(x, int):
-        return x, heads * D if stride is None else stride
-    if x.dim() != 3 or x.shape[0] < n or x.shape[1] != heads or x.shape[2] != D or x.stride(2) != 1 or x.stride(1) != D:
-        raise LkvError(LKV_ERR_INVALID_ARG, f"{what}: bf16 [{n}][{heads}][{D}] with heads side by side is wanted, "
-                                            f"not {tuple(x.shape)} with strides {x.stride()}")
-    # the stride of a single row means nothing to torch
-    return _want(what, x, "bfloat16", n * heads * D, contiguous=False), x.stride(0) if x.shape[0] > 1 else heads * D
+    rc = (_nat or native()).lkv_rope_table(spec, rows, table, stream)
+    if rc:
+        raise LkvError(rc, "lkv_rope_table")
 
 
 def lkv_rope_append_kv(spec, n_cap, Hq, Hkv, num_pages, page_tokens, D, n_tokens, positions, slots, q, k, v, q_weight,
@@ -361,50 +353,33 @@ def lkv_rope_append_kv(spec, n_cap, Hq, Hkv, num_pages, page_tokens, D, n_tokens
                        q_stride=None, k_stride=None, v_stride=None, reciprocal=False, stream=None):
     """q, k, v: bf16 [n_cap][heads][D], views of a fused projection among them (the strides are for integer
     addresses only)."""
-    w, spec = "lkv_rope_append_kv", _spec(spec)
-    q, q_stride = _token_rows(w, q, n_cap, Hq, D, q_stride)
-    k, k_stride = _token_rows(w, k, n_cap, Hkv, D, k_stride)
-    v, v_stride = _token_rows(w, v, n_cap, Hkv, D, v_stride)
-    kc, ksz, vc, vsz = _want_cache(w, spec, num_pages * Hkv * page_tokens, D, k_codes, k_sz, v_codes, v_sz)
-    _check(lib().lkv_rope_append_kv(spec, n_cap, Hq, Hkv, num_pages, page_tokens, D, _want(w, n_tokens, "int32", 1),
-                                    _want(w, positions, "int32", n_cap), _want(w, slots, "int64", n_cap), q, q_stride,
-                                    k, k_stride, v, v_stride, _want(w, q_weight, "bfloat16", D),
-                                    _want(w, k_weight, "bfloat16", D), eps, rot_dim, int(interleaved),
-                                    _want(w, table, "float32", table_rows * rot_dim), table_rows,
-                                    _want(w, q_out, "bfloat16", n_cap * Hq * D), kc, ksz, vc, vsz, int(reciprocal),
-                                    _stream(stream)), w)
+    rc = (_nat or native()).lkv_rope_append_kv(_spec(spec), n_cap, Hq, Hkv, num_pages, page_tokens, D, n_tokens,
+                                               positions, slots, q, q_stride, k, k_stride, v, v_stride, q_weight,
+                                               k_weight, eps, rot_dim, interleaved, table, table_rows, q_out, k_codes,
+                                               k_sz, v_codes, v_sz, reciprocal, stream)
+    if rc:
+        raise LkvError(rc, "lkv_rope_append_kv")
 
 
 def lkv_multi_workspace_bytes(spec, B, Hq, Hkv, T_cap, D, max_q):
     return lib().lkv_multi_workspace_bytes(_spec(spec), B, Hq, Hkv, T_cap, D, max_q)
 
 
-def _want_rule(what, rule, Hq, B):
-    for name, (x, dtype) in rule.tensors.items():
-        _want(what, x, dtype, Hq if name == "slopes" else B)
-    return rule
-
-
 def lkv_decode_attention_multi(spec, B, Hq, Hkv, T_cap, D, max_q, n_rows, seq_lens, cu_q, q, k_codes, k_sz, v_codes,
                                v_sz, rule, out, lse, workspace, ws_bytes, stream=None):
-    w, spec = "lkv_decode_attention_multi", _spec(spec)
-    cache = _want_cache(w, spec, B * Hkv * T_cap, D, k_codes, k_sz, v_codes, v_sz)
-    _check(lib().lkv_decode_attention_multi(spec, B, Hq, Hkv, T_cap, D, max_q, n_rows, _want(w, seq_lens, "int32", B),
-                                            _want(w, cu_q, "int32", B + 1), _want(w, q, "bfloat16", n_rows * Hq * D),
-                                            *cache, _want_rule(w, rule, Hq, B), _want(w, out, "float32", n_rows * Hq * D),
-                                            _want(w, lse, "float32", n_rows * Hq), _ptr(workspace), int(ws_bytes),
-                                            _stream(stream)), w)
+    rc = (_nat or native()).lkv_decode_attention_multi(_spec(spec), B, Hq, Hkv, T_cap, D, max_q, n_rows, seq_lens, cu_q,
+                                                       q, k_codes, k_sz, v_codes, v_sz, rule, out, lse, workspace,
+                                                       ws_bytes, stream)
+    if rc:
+        raise LkvError(rc, "lkv_decode_attention_multi")
 
 
 def lkv_decode_attention_multi_paged(spec, B, Hq, Hkv, pages_per_seq, num_pages, D, max_q, n_rows, seq_lens, cu_q, q,
                                      block_table, k_pool, k_sz_pool, v_pool, v_sz_pool, rule, out, lse, workspace,
                                      ws_bytes, stream=None):
-    w, spec = "lkv_decode_attention_multi_paged", _spec(spec)
-    cache = _want_cache(w, spec, num_pages * Hkv * LKV_PAGE_TOKENS, D, k_pool, k_sz_pool, v_pool, v_sz_pool)
-    _check(lib().lkv_decode_attention_multi_paged(spec, B, Hq, Hkv, pages_per_seq, num_pages, D, max_q, n_rows,
-                                                  _want(w, seq_lens, "int32", B), _want(w, cu_q, "int32", B + 1),
-                                                  _want(w, q, "bfloat16", n_rows * Hq * D),
-                                                  _want(w, block_table, "int32", B * pages_per_seq), *cache,
-                                                  _want_rule(w, rule, Hq, B), _want(w, out, "float32", n_rows * Hq * D),
-                                                  _want(w, lse, "float32", n_rows * Hq), _ptr(workspace), int(ws_bytes),
-                                                  _stream(stream)), w)
+    rc = (_nat or native()).lkv_decode_attention_multi_paged(_spec(spec), B, Hq, Hkv, pages_per_seq, num_pages, D, max_q,
+                                                             n_rows, seq_lens, cu_q, q, block_table, k_pool, k_sz_pool,
+                                                             v_pool, v_sz_pool, rule, out, lse, workspace, ws_bytes,
+                                                             stream)
+    if rc:
+        raise LkvError(rc, "lkv_decode_attention_multi_paged")

@@ -77,7 +77,7 @@ def test_served_up_to_the_first_that_does_not_fit(kw):
 
 
 def test_invalid_sequences_are_passed_over():
-    got, want = plan([-1, 5, 0, 1000, 2000000000, 7], [1, -3, 2, 25, 2000000000, 1], 4, list(range(9)))
+    got, want = plan([-1, 5, 0, 1000, 2000000000, 7], [1, -3, 2, 25, 2000000000, 1], 4, list(range(9)), n_cap=8)
     assert want["status"] == 1 and want["cu"][-1] == 3
     check(got, want)
 
