@@ -140,6 +140,7 @@ int lkv_page_plan(int B, int pages_per_seq, int num_pages, int n_cap, const int3
   a.lens = seq_lens; a.n_new = n_new; a.free_pages = free_pages; a.free_count = free_count;
   a.table = block_table; a.new_lens = new_lens; a.cu = cu_new; a.positions = positions; a.token_seq = token_seq;
   a.slots = slots; a.free_left = free_left; a.status = status;
+  a.wide = aligned16(positions) && aligned16(token_seq) && aligned16(slots);
   return from_cuda(launch_page_plan(a, static_cast<cudaStream_t>(stream)));
 }
 

@@ -53,8 +53,6 @@
 namespace lkv {
 namespace multi {
 
-using fused::hmma16816;
-using fused::hmma16816_bf16;
 using fused::hsub2_u32;
 using fused::kF16Magic2;
 
@@ -74,6 +72,35 @@ __device__ __forceinline__ float rcp(float x) {
   float y;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// mma.m16n8k16, fp32 accumulators (fragment layout: mma_k.cuh).  Pure functions
+// of their operands, so that independent products may be interleaved.
+__device__ __forceinline__ void hmma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                          uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void hmma16816_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                               uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The same from zero: c need not be cleared.
+__device__ __forceinline__ void hmma16816_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                                uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
+__device__ __forceinline__ void hmma16816_bf16_first(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                                     uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 
 // 2^n for an integer-valued n; 0 below the normal range.
@@ -280,7 +307,7 @@ __device__ __forceinline__ void load_unit(const MultiArgs& a, const Seq& s, int 
   const int r0 = w.rb * 8 * C::NT, r1 = min(r0 + 8 * C::NT, s.n * a.r);
   // what every row of the block sees, and what any row sees
   const int i0 = r0 / a.r, i1 = (r1 - 1) / a.r;
-  w.p_min = s.T - s.n + i0;
+  w.p_min = s.T - s.n + i0;  // below T
   w.p_max = s.T - s.n + i1;
   w.lo_min = max(s.start, a.window > 0 ? w.p_min - a.window + 1 : 0);
   w.lo_max = max(s.start, a.window > 0 ? w.p_max - a.window + 1 : 0);
@@ -468,6 +495,21 @@ __device__ __forceinline__ void ready_tokens(Work<C>& w, uint8_t* stage, uint32_
   __syncwarp();
 }
 
+// The (scale, zero) pairs of a token's NG groups.
+template <int NG>
+__device__ __forceinline__ void load_pairs(const float* p, float2 (&sz)[NG]) {
+  if constexpr (NG == 1) {
+    sz[0] = *reinterpret_cast<const float2*>(p);
+  } else {
+#pragma unroll
+    for (int i = 0; i < NG; i += 2) {
+      const float4 v = *reinterpret_cast<const float4*>(p + 2 * i);
+      sz[i] = make_float2(v.x, v.y);
+      sz[i + 1] = make_float2(v.z, v.w);
+    }
+  }
+}
+
 // ------------------------------------------------------------------ scores
 // Register J of a lane's 16 codes: two codes less the centre as exact fp16
 // values times 2^off, by the extraction plan of mma_k.cuh; at 16 bits the two
@@ -488,7 +530,7 @@ __device__ __forceinline__ uint32_t k_reg(const uint32_t (&word)[KB / 2], const 
   }
 }
 
-// acc[ts][group][nt] += K codes (rows = tokens 16 ts + gid, + 8) x q.
+// acc[group][nt] = K codes (rows = tokens 16 ts + gid, + 8) x q.
 template <typename C>
 __device__ __forceinline__ void k_product(const uint8_t* kc, const uint32_t* cen, const Work<C>& w, int ts,
                                           float (&acc)[C::AC][C::NT][4]) {
@@ -540,14 +582,25 @@ __device__ __forceinline__ void k_product(const uint8_t* kc, const uint32_t* cen
 #pragma unroll
       for (int nt = 0; nt < C::NT; ++nt) {
         const uint32_t b0 = w.qf[nt][blk][2 * ks], b1 = w.qf[nt][blk][2 * ks + 1];
+        // a group's first product starts its accumulator
+        constexpr int per = KB == 16 ? C::BLK : C::G == 32 ? 1 : C::BLK / C::NG;  // blocks of an accumulator
+        const bool start = ks == 0 && blk % per == 0;
         if constexpr (KB == 16) {
-          hmma16816_bf16(acc[0][nt], a0, a1, a2, a3, b0, b1);
+          if (start) hmma16816_bf16_first(acc[0][nt], a0, a1, a2, a3, b0, b1);
+          else hmma16816_bf16(acc[0][nt], a0, a1, a2, a3, b0, b1);
         } else if constexpr (C::G != 32) {
-          hmma16816(acc[blk * C::NG / C::BLK][nt], a0, a1, a2, a3, b0, b1);
+          if (start) hmma16816_first(acc[blk * C::NG / C::BLK][nt], a0, a1, a2, a3, b0, b1);
+          else hmma16816(acc[blk * C::NG / C::BLK][nt], a0, a1, a2, a3, b0, b1);
         } else {
           // lanes tig < 2 hold the block's first group of 32 channels, the others its second
-          hmma16816(acc[2 * blk][nt], a0, a1, a2, a3, tig < 2 ? b0 : 0u, tig < 2 ? b1 : 0u);
-          hmma16816(acc[2 * blk + 1][nt], a0, a1, a2, a3, tig < 2 ? 0u : b0, tig < 2 ? 0u : b1);
+          const uint32_t l0 = tig < 2 ? b0 : 0u, l1 = tig < 2 ? b1 : 0u, h0 = tig < 2 ? 0u : b0, h1 = tig < 2 ? 0u : b1;
+          if (start) {
+            hmma16816_first(acc[2 * blk][nt], a0, a1, a2, a3, l0, l1);
+            hmma16816_first(acc[2 * blk + 1][nt], a0, a1, a2, a3, h0, h1);
+          } else {
+            hmma16816(acc[2 * blk][nt], a0, a1, a2, a3, l0, l1);
+            hmma16816(acc[2 * blk + 1][nt], a0, a1, a2, a3, h0, h1);
+          }
         }
       }
     };
@@ -569,14 +622,18 @@ __device__ __forceinline__ void v_product(const uint8_t* vc, const float* vsz, W
   const float* szb = vsz + (16 * ts + tig) * C::NG * 2;
   constexpr int TERMS = VB == 16 ? 3 : 2;
   uint32_t pw[C::NT][TERMS][2];
+  float2 sz[4][C::NG];
+  if constexpr (VB < 16 && C::NG <= 2) {  // four groups at once would take 32 registers
+#pragma unroll
+    for (int j = 0; j < 4; ++j) load_pairs<C::NG>(szb + 4 * j * C::NG * 2, sz[j]);
+  }
 #pragma unroll
   for (int run = 0; run < C::RUNS; ++run) {
     if (run % C::GRUNS == 0) {
       const int gi = run / C::GRUNS;
-      float2 sz[4];
-      if constexpr (VB < 16) {
+      if constexpr (VB < 16 && C::NG > 2) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) sz[j] = *reinterpret_cast<const float2*>(szb + (4 * j * C::NG + gi) * 2);
+        for (int j = 0; j < 4; ++j) sz[j][gi] = *reinterpret_cast<const float2*>(szb + (4 * j * C::NG + gi) * 2);
       }
 #pragma unroll
       for (int nt = 0; nt < C::NT; ++nt) {
@@ -594,8 +651,8 @@ __device__ __forceinline__ void v_product(const uint8_t* vc, const float* vsz, W
         } else {
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            const float x = e[nt][2 * j] * sz[2 * j].x, y = e[nt][2 * j + 1] * sz[2 * j + 1].x;
-            w.zacc[nt][gi] = fmaf(e[nt][2 * j], sz[2 * j].y, fmaf(e[nt][2 * j + 1], sz[2 * j + 1].y, w.zacc[nt][gi]));
+            const float x = e[nt][2 * j] * sz[2 * j][gi].x, y = e[nt][2 * j + 1] * sz[2 * j + 1][gi].x;
+            w.zacc[nt][gi] = fmaf(e[nt][2 * j], sz[2 * j][gi].y, fmaf(e[nt][2 * j + 1], sz[2 * j + 1][gi].y, w.zacc[nt][gi]));
             const uint32_t h = pack_f16(x, y);
             const float2 f = unpack_f16(h);
             pw[nt][0][j] = h;
@@ -635,17 +692,11 @@ __device__ __forceinline__ void tile_step(const MultiArgs& a, Work<C>& w, uint8_
   const float* ksz = reinterpret_cast<const float*>(stage + C::OFF_KSZ);
   const float* vsz = reinterpret_cast<const float*>(stage + C::OFF_VSZ);
   const int t1 = t0 + C::TT - 1;
-  const bool whole = t1 < w.T && ((t0 >= w.lo_max && t1 <= w.p_min) || t1 < w.pre);
+  const bool whole = (t0 >= w.lo_max && t1 <= w.p_min) || t1 < w.pre;  // p_min and pre lie before T
   ready_tokens<C>(w, stage, cen, t0, whole);
 #pragma unroll
   for (int ts = 0; ts < TS; ++ts) {
     float acc[C::AC][NT][4];
-#pragma unroll
-    for (int i = 0; i < C::AC; ++i)
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][nt][j] = 0.0f;
     k_product<C>(stage, cen, w, ts, acc);
     // fold (scale, zero): rows gid and gid + 8, columns 2 tig and 2 tig + 1.  The
     // reference goes in before the one large rounding, so the scores that
@@ -659,9 +710,7 @@ __device__ __forceinline__ void tile_step(const MultiArgs& a, Work<C>& w, uint8_
     } else {
       float2 sz[2][NG];
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int gi = 0; gi < NG; ++gi) sz[i][gi] = *reinterpret_cast<const float2*>(ksz + ((16 * ts + gid + 8 * i) * NG + gi) * 2);
+      for (int i = 0; i < 2; ++i) load_pairs<NG>(ksz + (16 * ts + gid + 8 * i) * NG * 2, sz[i]);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -892,11 +941,14 @@ struct Feed {
   int t0, T, edge, to;         // its first token; behind the prefix tiles, at edge, comes to
   int cnt, units, rbs, begin;  // rbs: row blocks of a KV head; begin: first token of a unit
   long long base;              // contiguous: the head's first row; paged: the sequence's first table entry
+  long long page_row;          // paged: the head's first row of the page at hand, less that page's first token
+  int page;                    // its place in the table, -1: none yet
   bool fresh;                  // the warp's first tile of the unit
 };
 
 __device__ __forceinline__ void feed_base(const MultiArgs& a, Feed& f) {
   f.base = a.table == nullptr ? ((long long)f.b * a.Hkv + f.ui / f.rbs) * a.T_cap : (long long)f.b * a.pps;
+  f.page = -1;
 }
 
 template <int NT, int TT>
@@ -937,7 +989,7 @@ constexpr int kFresh = 1 << 8, kEnd = 1 << 9;
 
 // Start the copies of a tile into a stage, one lane each; the bytes complete on bar.
 template <typename C>
-__device__ __forceinline__ void fetch_tile(const MultiArgs& a, const Feed& f, uint8_t* stage, int4* what, uint64_t* bar,
+__device__ __forceinline__ void fetch_tile(const MultiArgs& a, Feed& f, uint8_t* stage, int4* what, uint64_t* bar,
                                            const uint8_t* src, int row_bytes, int off, uint64_t policy) {
   const int lane = threadIdx.x & 31;
   int n = max(0, min(C::TT, f.T - f.t0));
@@ -945,16 +997,18 @@ __device__ __forceinline__ void fetch_tile(const MultiArgs& a, const Feed& f, ui
   if (n > 0) {
     // (scale, zero) rows of 8 bytes go in pairs; the capacity is even then
     if constexpr ((C::NG & 1) && (C::KB < 16 || C::VB < 16)) n += n & 1;
-    long long row;
-    if (a.table == nullptr) {
-      row = f.base + f.t0;
-    } else {
-      int page = __ldg(a.table + f.base + f.t0 / kPageTokens);
-      if (page < 0 || page >= a.num_pages) {
-        if (lane == 0) atomicMax(a.status, kStatusInvalidArg);
-        page = 0;
+    long long row = f.base + f.t0;
+    if (a.table != nullptr) {
+      if (f.t0 / kPageTokens != f.page) {
+        f.page = f.t0 / kPageTokens;
+        int page = __ldg(a.table + f.base + f.page);
+        if (page < 0 || page >= a.num_pages) {
+          if (lane == 0) atomicMax(a.status, kStatusInvalidArg);
+          page = 0;
+        }
+        f.page_row = (((long long)page * a.Hkv + f.ui / f.rbs) - f.page) * kPageTokens;
       }
-      row = ((long long)page * a.Hkv + f.ui / f.rbs) * kPageTokens + f.t0 % kPageTokens;
+      row = f.page_row + f.t0;
     }
     constexpr int all = C::KRB + C::VRB + (C::KB < 16 ? C::NG * 8 : 0) + (C::VB < 16 ? C::NG * 8 : 0);
     if (lane == 0) mbar_arrive_expect_tx(bar, n * all);
@@ -1093,9 +1147,55 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) multi_kernel(MultiArgs a) {
   const int ctas = min((int)gridDim.x, (total + W - 1) / W);
   const int cta = blockIdx.x;
   if (cta >= ctas) return;
-  auto cta_begin = [&](int c) { return (int)((long long)total * c / ctas); };
+  // equal runs: the first `rem` of them one longer
+  const int q0 = total / ctas, rem0 = total - q0 * ctas;
+  auto cta_begin = [&](int c) { return c * q0 + min(c, rem0); };
   const int x0 = cta_begin(cta), x1 = cta_begin(cta + 1);
-  auto warp_begin = [&](int w) { return x0 + (int)((long long)(x1 - x0) * w / W); };
+  const int q1 = (x1 - x0) / W, rem1 = (x1 - x0) - q1 * W;
+  auto warp_begin = [&](int w) { return x0 + w * q1 + min(w, rem1); };
+
+  // Units cut by a run end: one lane per boundary finds its unit.  By one warp, while its first copies are under way.
+  auto cta_of = [&](int x) { return x < rem0 * (q0 + 1) ? x / (q0 + 1) : rem0 + (x - rem0 * (q0 + 1)) / q0; };
+  auto find_cuts = [&]() {
+    if (lane <= W) s_begin[lane] = lane < W ? warp_begin(lane) : x1;
+    Cut u{};
+    bool cut = false;
+    if (lane <= W) {
+      const int x = lane < W ? warp_begin(lane) : x1;
+      if (x < total) {
+        const Place p = seek<NT, TT>(a, first, x);
+        u.u0 = x - p.ti;
+        u.u1 = u.u0 + p.s.cnt;
+        const int rbs = p.s.units / a.Hkv;
+        u.g = p.ui / rbs;
+        u.row0 = (p.ui - u.g * rbs) * 8 * NT;
+        u.rows = min(8 * NT, p.s.n * a.r - u.row0);
+        u.c0 = p.s.c0;
+        cut = u.u0 < x;
+      }
+    }
+    // boundaries rise, so equal units stand side by side (among those that cut)
+    const unsigned cuts = __ballot_sync(kFull, cut);
+    const unsigned below = cuts & ((1u << lane) - 1u);
+    const int prev = below ? 31 - __clz(below) : 0;
+    const int pu = __shfl_sync(kFull, u.u0, prev);
+    const bool lead = cut && (!below || pu != u.u0);
+    const unsigned leads = __ballot_sync(kFull, lead);
+    if (lead) {
+      // its pieces: the runs that reach past its begin and start before its end
+      u.k0 = 0;
+      u.k1 = W;
+      while (warp_begin(u.k0 + 1) <= u.u0) ++u.k0;
+      while (warp_begin(u.k1 - 1) >= u.u1) --u.k1;
+      if (u.u0 < x0 || u.u1 > x1) {
+        u.ck0 = cta_of(u.u0);
+        u.ck1 = cta_of(u.u1 - 1) + 1;
+        u.slot = u.u0 > cta_begin(u.ck0) ? 1 : 0;
+      }
+      s_cut[__popc(leads & ((1u << lane) - 1u))] = u;
+    }
+    if (lane == 0) { s_ncut = __popc(leads); s_last[0] = s_last[1] = 0; }
+    };
 
   float* const early = a.pieces + (long long)cta * W * PF;  // pieces of units that end inside a run, one per warp
   static_assert(PF * 4 <= ST * C::STAGE, "a run's last piece fits its ring");
@@ -1120,6 +1220,7 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) multi_kernel(MultiArgs a) {
         fetch_tile<C>(a, f, ring + i * C::STAGE, what + i, bar + i, src, row_bytes, off, policy);
       }
       __syncwarp();
+      if (warp == W - 1) find_cuts();
       Work<C> w;
       bool dead = false;
       int st = 0;
@@ -1159,6 +1260,7 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) multi_kernel(MultiArgs a) {
       if (dead)
         for (int i = 0; i < ST; ++i) mbar_wait(bar + i, parity >> i & 1, 1000000ull);
     } else {
+      if (warp == W - 1) find_cuts();
       // a run without tiles (fewer tiles than warps) leaves an empty piece
       float* piece = reinterpret_cast<float*>(ring);
       for (int i = lane; i < PF; i += 32) piece[i] = i < 16 * NT && !(i & 1) ? -INFINITY : 0.0f;
@@ -1166,48 +1268,6 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) multi_kernel(MultiArgs a) {
   }
   __syncthreads();
 
-  // ---- units cut by a run end: one lane per boundary finds its unit
-  auto cta_of = [&](int x) { return (int)((((long long)x + 1) * ctas - 1) / total); };
-  if (tid <= W) s_begin[tid] = tid < W ? warp_begin(tid) : x1;
-  if (warp == 0) {
-    Cut u{};
-    bool cut = false;
-    if (lane <= W) {
-      const int x = lane < W ? warp_begin(lane) : x1;
-      if (x < total) {
-        const Place p = seek<NT, TT>(a, first, x);
-        u.u0 = x - p.ti;
-        u.u1 = u.u0 + p.s.cnt;
-        const int rbs = p.s.units / a.Hkv;
-        u.g = p.ui / rbs;
-        u.row0 = (p.ui - u.g * rbs) * 8 * NT;
-        u.rows = min(8 * NT, p.s.n * a.r - u.row0);
-        u.c0 = p.s.c0;
-        cut = u.u0 < x;
-      }
-    }
-    // boundaries rise, so equal units stand side by side (among those that cut)
-    const unsigned cuts = __ballot_sync(kFull, cut);
-    const unsigned below = cuts & ((1u << lane) - 1u);
-    const int prev = below ? 31 - __clz(below) : 0;
-    const int pu = __shfl_sync(kFull, u.u0, prev);
-    const bool lead = cut && (!below || pu != u.u0);
-    const unsigned leads = __ballot_sync(kFull, lead);
-    if (lead) {
-      // its pieces: the runs that reach past its begin and start before its end
-      u.k0 = 0;
-      u.k1 = W;
-      while (warp_begin(u.k0 + 1) <= u.u0) ++u.k0;
-      while (warp_begin(u.k1 - 1) >= u.u1) --u.k1;
-      if (u.u0 < x0 || u.u1 > x1) {
-        u.ck0 = cta_of(u.u0);
-        u.ck1 = cta_of(u.u1 - 1) + 1;
-        u.slot = u.u0 > cta_begin(u.ck0) ? 1 : 0;
-      }
-      s_cut[__popc(leads & ((1u << lane) - 1u))] = u;
-    }
-    if (lane == 0) { s_ncut = __popc(leads); s_last[0] = s_last[1] = 0; }
-  }
   __syncthreads();
   const int ncut = s_ncut;
   if (ncut == 0) return;

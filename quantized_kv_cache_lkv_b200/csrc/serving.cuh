@@ -13,6 +13,7 @@ struct PlanArgs {
   int32_t *table, *new_lens, *cu, *positions, *token_seq;
   int64_t* slots;
   int32_t *free_left, *status;
+  bool wide;  // positions, token_seq and slots are 16-byte aligned
 };
 
 struct RopeTableArgs {

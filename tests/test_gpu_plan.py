@@ -90,6 +90,20 @@ def test_page_ids_out_of_range_give_no_slot():
     check(got, want)
 
 
+def test_unaligned_outputs():
+    """Token rows that start 4 or 8 bytes off a 16-byte boundary."""
+    lens, new, free = draw(9, 5, 900, 200, 5)
+    n_cap = int(new.sum()) + 1
+    buf = [torch.full((n_cap + 1,), -7, dtype=d, device="cuda") for d in (torch.int32, torch.int32, torch.int64)]
+    o = {"table": cu32((7000 + np.arange(45)).reshape(9, 5)), "new_lens": cu32([0] * 9), "cu": cu32([0] * 10), "left": cu32([0]),
+         "status": cu32([0]), "pos": buf[0][1:], "seq": buf[1][1:], "slots": buf[2][1:]}
+    want = ref.page_plan(lens, new, list(free), len(free), (7000 + np.arange(45)).reshape(9, 5), 1 << 20, n_cap)
+    lkv.lkv_page_plan(9, 5, 1 << 20, n_cap, cu32(lens), cu32(new), cu32(free), len(free), cu32([len(free)]), o["table"], o["new_lens"],
+                      o["cu"], o["pos"], o["seq"], o["slots"], o["left"], o["status"])
+    check({k: v.cpu().numpy() for k, v in o.items()}, want)
+    assert all(int(x[0]) == -7 for x in buf)
+
+
 def test_no_sequences():
     check(*plan([], [], 4, [1, 2]))
 
