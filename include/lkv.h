@@ -413,7 +413,7 @@ LKV_API int lkv_tiered_decode(int B, int Hq, int Hkv, int T_cap, int D, int grou
  *                     some sequence was invalid or not served, or a page id
  *                     was out of range
  *
- * At most 16384 sequences (LKV_ERR_UNSUPPORTED).  No output may overlap an
+ * At most 16384 sequences and n_cap 2^30 (LKV_ERR_UNSUPPORTED).  No output may overlap an
  * input or another output (LKV_ERR_INVALID_ARG): every block reads all the
  * lengths, so new_lens must be another buffer than seq_lens.
  */
@@ -512,7 +512,7 @@ LKV_API int lkv_rope_append_kv(lkv_qspec spec, int n_cap, int Hq, int Hkv, int n
 /* Scores and visibility of lkv_decode_attention_multi. */
 typedef struct {
     float softmax_scale;        /* finite */
-    float softcap;              /* c > 0: scores become c * tanh(score / c); 0: none */
+    float softcap;              /* c >= 1e-30: scores become c * tanh(score / c); 0: none */
     int32_t window;             /* w > 0: a query sees the last w positions, its own among them; 0: all */
     const float *slopes;        /* device f32 [Hq], nullable: slopes[h] * (t - p) is added to the score */
     const int32_t *prefix_lens; /* device int32 [B], nullable: positions before it are visible to every query */

@@ -45,6 +45,8 @@ int multi_impl(lkv_qspec spec, int B, int Hq, int Hkv, int T_cap, int D, int max
   if (n_rows < 0 || (cu_q == nullptr && n_rows < B)) return LKV_ERR_INVALID_ARG;
   if (!std::isfinite(rule.softmax_scale) || !std::isfinite(rule.softcap) || rule.softcap < 0.0f || rule.window < 0)
     return LKV_ERR_INVALID_ARG;
+  // scores are divided by the cap: a smaller one takes them out of fp32
+  if (rule.softcap > 0.0f && rule.softcap < 1e-30f) return LKV_ERR_INVALID_ARG;
   if (!int_ptr_ok(rule.slopes, false) || !int_ptr_ok(rule.prefix_lens, false) || !int_ptr_ok(rule.doc_starts, false) ||
       !int_ptr_ok(cu_q, false) || !int_ptr_ok(lse, false) || !int_ptr_ok(seq_lens, B > 0))
     return LKV_ERR_INVALID_ARG;
@@ -117,7 +119,7 @@ int lkv_page_plan(int B, int pages_per_seq, int num_pages, int n_cap, const int3
                   int32_t* new_lens, int32_t* cu_new, int32_t* positions, int32_t* token_seq, int64_t* slots,
                   int32_t* free_left, int32_t* status, void* stream) {
   if (B < 0 || n_cap < 0 || free_cap < 0 || pages_per_seq <= 0 || num_pages <= 0) return LKV_ERR_INVALID_ARG;
-  if (B > kPlanMaxBatch || (long long)pages_per_seq * kPageTokens > (1ll << 30)) return LKV_ERR_UNSUPPORTED;
+  if (B > kPlanMaxBatch || n_cap > (1 << 30) || (long long)pages_per_seq * kPageTokens > (1ll << 30)) return LKV_ERR_UNSUPPORTED;
   const bool b = B > 0, t = n_cap > 0;
   if (!int_ptr_ok(seq_lens, b) || !int_ptr_ok(n_new, b) || !int_ptr_ok(free_pages, free_cap > 0) ||
       !int_ptr_ok(free_count, true) || !int_ptr_ok(block_table, b) || !int_ptr_ok(new_lens, b) || !int_ptr_ok(cu_new, true) ||

@@ -12,6 +12,7 @@
 #include <algorithm>
 #include <cmath>
 
+#include "api_common.cuh"
 #include "serving.cuh"
 
 namespace lkv {
@@ -22,55 +23,62 @@ constexpr int kThreads = 256;
 constexpr int kRun = 32;      // rows of one thread
 constexpr int kMaxHalf = 64;  // rot_dim <= 128
 
-// The frequency of pair i.
-__device__ double frequency(const RopeTableArgs& a, int i) {
-  const double f = exp2(-log2(a.base) * (double)i / (double)a.half);
-  const double two_pi = 6.283185307179586476925286766559;
-  if (a.kind == 1) return f / a.factor;
-  if (a.kind == 2) {  // by turns inside the original context
-    const double g = (a.orig * f / two_pi - a.low) / (a.high - a.low);
-    const double mix = fmin(fmax(g, 0.0), 1.0);
-    return (1.0 - mix) * (f / a.factor) + mix * f;
+// The frequency of each pair, made on the host (a few fp64 functions in a row
+// would be half of a small table's time on the device).
+struct Frequencies {
+  double f[kMaxHalf];
+};
+
+Frequencies frequencies(const RopeTableArgs& a) {
+  const double two_pi = 6.283185307179586476925286766559, rot = 2.0 * a.half, log_base = std::log(a.base);
+  // the ramp's ends, by dimension
+  double lo = 0.0, hi = 0.0;
+  if (a.kind == LKV_ROPE_RAMP) {
+    lo = std::max(std::floor(rot * std::log(a.orig / (a.high * two_pi)) / (2.0 * log_base)), 0.0);
+    hi = std::min(std::ceil(rot * std::log(a.orig / (a.low * two_pi)) / (2.0 * log_base)), rot - 1.0);
   }
-  if (a.kind == 3) {  // by dimension
-    const double rot = 2.0 * a.half;
-    const double lo = fmax(floor(rot * log(a.orig / (a.high * two_pi)) / (2.0 * log(a.base))), 0.0);
-    const double hi = fmin(ceil(rot * log(a.orig / (a.low * two_pi)) / (2.0 * log(a.base))), rot - 1.0);
-    const double mix = fmin(fmax(((double)i - lo) / fmax(hi - lo, 0.001), 0.0), 1.0);
-    return f / a.factor * mix + f * (1.0 - mix);
+  Frequencies fr{};
+  for (int i = 0; i < a.half; ++i) {
+    const double f = std::exp(-log_base * i / a.half);
+    double mix = 1.0;  // share of the unscaled frequency
+    if (a.kind == LKV_ROPE_LINEAR) mix = 0.0;
+    if (a.kind == LKV_ROPE_SMOOTH) mix = std::min(std::max((a.orig * f / two_pi - a.low) / (a.high - a.low), 0.0), 1.0);
+    if (a.kind == LKV_ROPE_RAMP) mix = 1.0 - std::min(std::max((i - lo) / std::max(hi - lo, 0.001), 0.0), 1.0);
+    fr.f[i] = mix == 1.0 ? f : (1.0 - mix) * (f / a.factor) + mix * f;
   }
-  return f;
+  return fr;
 }
 
 __device__ __forceinline__ double2 turn(double2 x, double2 y) {
   return make_double2(x.x * y.x - x.y * y.y, x.y * y.x + x.x * y.y);
 }
 
-__global__ void __launch_bounds__(kThreads) rope_table_kernel(RopeTableArgs a, int slabs) {
+__global__ void __launch_bounds__(kThreads) rope_table_kernel(float* table, double attn, int half, int rows, int slabs,
+                                                              const __grid_constant__ Frequencies fr) {
   __shared__ double2 s_base[kMaxHalf], s_slab[kMaxHalf], s_one[kMaxHalf];
   const int tid = threadIdx.x;
   const long long p0 = (long long)blockIdx.x * slabs * kRun;
   // one evaluation a thread: three angles of each pair
-  if (tid < 3 * a.half) {
-    const int i = tid % a.half, which = tid / a.half;
-    const double f = frequency(a, i);
+  if (tid < 3 * half) {
+    const int i = tid % half, which = tid / half;
+    const double f = fr.f[i];
     double2 v;
     sincos(f * (which == 0 ? (double)p0 : which == 1 ? (double)kRun : 1.0), &v.y, &v.x);
-    if (which == 0) s_base[i] = make_double2(v.x * a.attn, v.y * a.attn);
+    if (which == 0) s_base[i] = make_double2(v.x * attn, v.y * attn);
     else if (which == 1) s_slab[i] = v;
     else s_one[i] = v;
   }
   __syncthreads();
-  const int i = tid % a.half, slab = tid / a.half;
+  const int i = tid % half, slab = tid / half;
   if (slab >= slabs) return;
   double2 v = s_base[i];
   const double2 by = s_slab[i], one = s_one[i];
   for (int k = 0; k < slab; ++k) v = turn(v, by);
   long long p = p0 + (long long)slab * kRun;
-  const long long end = p + kRun < a.rows ? p + kRun : a.rows;
-  float2* dst = reinterpret_cast<float2*>(a.table) + p * a.half + i;
+  const long long end = p + kRun < rows ? p + kRun : rows;
+  float2* dst = reinterpret_cast<float2*>(table) + p * half + i;
 #pragma unroll 4
-  for (; p < end; ++p, dst += a.half) {
+  for (; p < end; ++p, dst += half) {
     *dst = make_float2((float)v.x, (float)v.y);
     v = turn(v, one);
   }
@@ -83,7 +91,7 @@ cudaError_t launch_rope_table(const RopeTableArgs& a, cudaStream_t s) {
   const int slabs = std::max(1, std::min(kThreads / a.half, 8));
   const long long rows = (long long)slabs * kRun;
   const long long blocks = (a.rows + rows - 1) / rows;
-  rope_table_kernel<<<(unsigned)blocks, kThreads, 0, s>>>(a, slabs);
+  rope_table_kernel<<<(unsigned)blocks, kThreads, 0, s>>>(a.table, a.attn, a.half, a.rows, slabs, frequencies(a));
   return cudaGetLastError();
 }
 

@@ -42,7 +42,7 @@ def plan_args(**kw):
 
 @pytest.mark.parametrize("kw,want", [
     (dict(B=-1), ARG), (dict(n_cap=-1), ARG), (dict(free_cap=-1), ARG), (dict(pages_per_seq=0), ARG), (dict(num_pages=0), ARG),
-    (dict(B=16385), UNSUPPORTED), (dict(pages_per_seq=(1 << 22) + 1), UNSUPPORTED),
+    (dict(B=16385), UNSUPPORTED), (dict(n_cap=(1 << 30) + 1), UNSUPPORTED), (dict(pages_per_seq=(1 << 22) + 1), UNSUPPORTED),
     (dict(seq_lens=None), ARG), (dict(n_new=None), ARG), (dict(free_pages=None), ARG), (dict(free_count=None), ARG),
     (dict(block_table=None), ARG), (dict(new_lens=None), ARG), (dict(cu_new=None), ARG), (dict(positions=None), ARG),
     (dict(token_seq=None), ARG), (dict(slots=None), ARG), (dict(free_left=None), ARG),
@@ -113,7 +113,7 @@ MULTI = [
     (dict(spec=(6, 3, 64)), UNSUPPORTED), (dict(D=256), UNSUPPORTED), (dict(Hq=7), ARG), (dict(Hq=0), ARG), (dict(Hkv=0), ARG), (dict(B=-1), ARG),
     (dict(Hq=130), UNSUPPORTED), (dict(max_q=0), ARG), (dict(max_q=65), UNSUPPORTED), (dict(B=4097), UNSUPPORTED), (dict(n_rows=-1), ARG),
     (dict(cu_q=None, n_rows=1), ARG), (dict(rule=rule(softmax_scale=float("inf"))), ARG), (dict(rule=rule(softcap=-1.0)), ARG),
-    (dict(rule=rule(softcap=float("nan"))), ARG), (dict(rule=rule(window=-1)), ARG), (dict(rule=rule(slopes=FAKE + 2)), ARG),
+    (dict(rule=rule(softcap=float("nan"))), ARG), (dict(rule=rule(softcap=1e-31)), ARG), (dict(rule=rule(window=-1)), ARG), (dict(rule=rule(slopes=FAKE + 2)), ARG),
     (dict(rule=rule(prefix_lens=FAKE + 1)), ARG), (dict(rule=rule(doc_starts=FAKE + 3)), ARG), (dict(seq_lens=None), ARG), (dict(q=None), ARG),
     (dict(q=at(2) + 8), ARG), (dict(out=None), ARG), (dict(lse=at(8) + 2), ARG), (dict(k_codes=None), ARG), (dict(k_sz=None), ARG),
     (dict(v_codes=at(5) + 4), ARG), (dict(v_sz=None), ARG), (dict(cu_q=at(1) + 2), ARG), (dict(workspace=None), ARG), (dict(workspace=at(9) + 128), ARG),

@@ -220,6 +220,83 @@ def test_q_of_zeros_and_tiny_and_large(orc):
         close(out.cpu().numpy(), want, cache.vmax, f"scale {scale}")
 
 
+def from_values(orc, kb, vb, G, k, v, lens):
+    """A contiguous cache of given bf16 K and V [B][Hkv][T][D]."""
+    c = Cache.__new__(Cache)
+    D = k.shape[-1]
+    p = orc.quantize_kv(kb, vb, G, W.bf16_bits(k), W.bf16_bits(v), np.full(k.shape[0], k.shape[2], np.int32))
+    c.kb, c.vb, c.G, c.T_cap, c.lens, c.table, c.host = kb, vb, G, k.shape[2], lens, None, p
+    c.khat = orc.dequant_rows(p["k_codes"], p["k_sz"], D, G, kb)
+    c.vhat = orc.dequant_rows(p["v_codes"], p["v_sz"], D, G, vb)
+    c.vmax = float(np.abs(c.vhat).max())
+    c.t = {key: torch.from_numpy(x).cuda() for key, x in p.items()}
+    return c
+
+
+@pytest.mark.parametrize("kb,vb,G", [(6, 4, 64), (8, 8, 32), (4, 2, 128), (2, 6, 64)])
+@pytest.mark.parametrize("how", ["constant", "rising", "tiny", "huge", "offset"])
+def test_ranges_of_v_and_k(orc, kb, vb, G, how):
+    """Groups without a range, V whose scales rise by 2^40 along the sequence, V near the ends of fp32, and values far
+    from 0 next to their range."""
+    gen = torch.Generator().manual_seed(5)
+    B, Hkv, T, D = 2, 1, 400, 128
+    k, v = torch.randn(B, Hkv, T, D, generator=gen), torch.randn(B, Hkv, T, D, generator=gen)
+    if how == "constant":
+        k, v = k[..., :1].expand_as(k).clone(), v[..., :1].expand_as(v).clone()
+    if how == "rising":
+        v = v * torch.exp2(torch.arange(T) * 0.1)[:, None]
+    if how == "tiny":
+        v = v * 2.0 ** -100
+    if how == "huge":
+        v = v * 2.0 ** 100
+    if how == "offset":
+        k, v = k + 5.0, v * 0.01 + 30.0
+    cache = from_values(orc, kb, vb, G, k.to(torch.bfloat16), v.to(torch.bfloat16), (T, 33))
+    q = make_q(2, 8, D, 6)
+    out, lse, _ = call(cache, q.cuda(), None, lkv.lkv_score_rule(D ** -0.5), 1)
+    want, wl = ref.attention(q.float().numpy(), cache.khat, cache.vhat, (T, 33), None, float(np.float32(D ** -0.5)))
+    close(out.cpu().numpy(), want, cache.vmax, how)
+    close_lse(lse.cpu().numpy(), wl)
+
+
+def test_no_capacity():
+    """T_cap 0: nothing to see, zeros."""
+    out, lse = torch.full((2, 8, 128), 5.0, device="cuda"), torch.full((2, 8), 5.0, device="cuda")
+    ws = buffers.alloc_workspace(lkv.lkv_multi_workspace_bytes((6, 4, 64), 2, 8, 2, 0, 128, 1))
+    lkv.lkv_decode_attention_multi((6, 4, 64), 2, 8, 2, 0, 128, 1, 2, cu32([0, 0]), None, make_q(2, 8, 128, 1).cuda(), None, None, None, None,
+                                   lkv.lkv_score_rule(0.1), out, lse, ws, ws.numel())
+    assert (out == 0).all() and torch.isneginf(lse).all()
+
+
+def test_largest_batch(orc):
+    """4096 sequences, most of them short."""
+    rng = np.random.default_rng(8)
+    case(orc, 4, 4, 64, lens=tuple(int(x) for x in rng.integers(0, 20, 4096)), Hkv=1, r=1, D=64, seed=52)
+
+
+def test_two_calls_at_once_with_their_own_workspaces(orc):
+    """Two streams, two workspaces: each call's result is what it is alone."""
+    one = case(orc, lens=(4000, 900), n=2, seed=71)
+    two = case(orc, 8, 4, 64, lens=(2500, 1, 3000), r=8, seed=72)
+    s, t = torch.cuda.Stream(), torch.cuda.Stream()
+    got, keep = [], []
+    for _ in range(3):
+        for stream, (cache, q, cu, rule, out, lse, ws) in ((s, one), (t, two)):
+            rows, Hq, D = q.shape
+            o = torch.full_like(out, 5.0)
+            c, max_q = cache.t, 2 if cache is one[0] else 1
+            lens, offsets, qd = cu32(cache.lens), cu32(cu), q.cuda()
+            keep += [lens, offsets, qd]  # until both streams are done with them
+            stream.wait_stream(torch.cuda.current_stream())
+            lkv.lkv_decode_attention_multi((cache.kb, cache.vb, cache.G), len(cache.lens), Hq, 2, cache.T_cap, D, max_q, rows,
+                                           lens, offsets, qd, c["k_codes"], c["k_sz"], c["v_codes"], c["v_sz"], rule, o,
+                                           None, ws, ws.numel(), stream=stream)
+            got.append((o, out))
+    torch.cuda.synchronize()
+    for o, want in got:
+        assert torch.equal(o, want)
+
+
 def test_same_result_every_time_and_on_a_used_workspace(orc):
     """Bit-identical on a workspace that calls of other sizes have used, on another stream, and without lse."""
     cache, q, cu, rule, out, lse, _ = case(orc, lens=(5000, 40, 3000), n=3, seed=61)
