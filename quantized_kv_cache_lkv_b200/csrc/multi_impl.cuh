@@ -299,15 +299,15 @@ struct Work {
   int p[C::NT], lo[C::NT];         // row gid: position of its token, first visible token behind the prefix
   float slope[C::NT];
   bool on[C::NT];
-  int b, ui, g, rb, T, c0, n, pre, p_min, p_max, lo_min, lo_max;  // the unit
+  int g, rb, T, c0, n, pre, p_min, p_max, lo_min, lo_max;  // the unit
 };
 
 // q of the unit's rows as B fragments, and the factors of the affine part.
 template <typename C>
-__device__ __forceinline__ void load_unit(const MultiArgs& a, const Seq& s, int b, int ui, Work<C>& w) {
+__device__ __forceinline__ void load_unit(const MultiArgs& a, const Seq& s, int ui, Work<C>& w) {
   const int lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
   const int rbs = s.units / a.Hkv;
-  w.b = b; w.ui = ui; w.g = ui / rbs; w.rb = ui % rbs;
+  w.g = ui / rbs; w.rb = ui % rbs;
   w.T = s.T; w.c0 = s.c0; w.n = s.n; w.pre = s.pre;
   const int r0 = w.rb * 8 * C::NT, r1 = min(r0 + 8 * C::NT, s.n * a.r);
   // what every row of the block sees, and what any row sees
@@ -427,9 +427,9 @@ constexpr float kRound = 12582912.0f;       // 1.5 * 2^23: adding it rounds to a
 constexpr uint32_t kRoundBits = 0x4B400000u;
 
 // The lane of a token readies its (scale, zero) rows: K's zero becomes the
-// value of the code nearest 0 (the code itself goes to cen), V's that of the middle code, and V's scale is taken relative
-// to w.top, which is raised (and the output rescaled) when a scale passes it.
-// What no row sees becomes 0 in V.
+// value of the code nearest 0 (the code itself goes to cen), V's that of the
+// middle code, and V's scale is taken relative to w.top, which is raised (and
+// the output rescaled) when a scale passes it.  What no row sees becomes 0 in V.
 template <typename C>
 __device__ __forceinline__ void ready_tokens(Work<C>& w, uint8_t* stage, uint32_t* cen, int t0, bool whole) {
   const int lane = threadIdx.x & 31;
@@ -1018,17 +1018,13 @@ __device__ __forceinline__ void fetch_tile(const MultiArgs& a, Feed& f, uint8_t*
     constexpr int all = C::KRB + C::VRB + (C::KB < 16 ? C::NG * 8 : 0) + (C::VB < 16 ? C::NG * 8 : 0);
     if (lane == 0) mbar_arrive_expect_tx(bar, n * all);
     __syncwarp();
-    if (lane < 4 && row_bytes > 0) {
-      bulk_g2s(stage + off, src + row * row_bytes, n * row_bytes, bar, policy);
-    }
+    if (lane < 4 && row_bytes > 0) bulk_g2s(stage + off, src + row * row_bytes, n * row_bytes, bar, policy);
   }
 }
 
-// Joining the pieces k0 .. k1 - 1 of a cut unit; at(k) is where piece k lies.
-// First the weights 2^(ref_k - max) of a row, then the sums of the outputs,
-// whose loads do not depend on one another.
-
-// Pieces of other CTAs are read past L1.
+// Joining the pieces p0 .. p1 - 1 of a cut unit (at(k) is where piece k lies):
+// first the weights 2^(ref_k - max) of a row, then the sums of the outputs,
+// whose loads do not depend on one another.  Pieces of other CTAs are read past L1.
 template <bool L2, typename T>
 __device__ __forceinline__ T ld(const T* p) {
   if constexpr (L2) return __ldcg(p);
@@ -1200,7 +1196,7 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) multi_kernel(MultiArgs a) {
       s_cut[__popc(leads & ((1u << lane) - 1u))] = u;
     }
     if (lane == 0) { s_ncut = __popc(leads); s_last[0] = s_last[1] = 0; }
-    };
+  };
 
   float* const early = a.pieces + (long long)cta * W * PF;  // pieces of units that end inside a run, one per warp
   static_assert(PF * 4 <= ST * C::STAGE, "a run's last piece fits its ring");
@@ -1234,7 +1230,7 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) multi_kernel(MultiArgs a) {
         const int4 d = what[st];
         uint8_t* stage = ring + st * C::STAGE;
         if (d.y & kFresh) {
-          load_unit<C>(a, load_seq<NT, TT>(a, d.z), d.z, d.w, w);
+          load_unit<C>(a, load_seq<NT, TT>(a, d.z), d.w, w);
           here = here || x > w0;
         }
         if (d.y & 0xFF) {
