@@ -4,10 +4,11 @@
 // A decode step makes a few of these calls for every layer, so what the host
 // spends on one counts: type, size, contiguity and device of a dozen tensors
 // cost about 8 microseconds checked from Python and a tenth of that here.
-// Module functions take the arguments of the C calls in their order, the
-// stream last (None: torch's current one), and return the lkv_status; a
-// tensor that does not fit raises LkvError with LKV_ERR_INVALID_ARG.  Integer
-// arguments in a tensor's place are device addresses and go through unchecked.
+// Module functions take the arguments of the C calls by position or name, the
+// stream last (None: torch's current one).  A nonzero lkv_status raises
+// LkvError, and so does a tensor that does not fit (LKV_ERR_INVALID_ARG).
+// Integer arguments in a tensor's place are device addresses and go through
+// unchecked.
 // The entry points' addresses come from the loaded liblkv.so (connect()).
 #include <torch/csrc/autograd/python_variable.h>
 
@@ -34,14 +35,58 @@ struct Entries {
 
 struct Failed {};  // a Python error is set
 
+void raise(int status, const char* what) {
+  PyObject* e = PyObject_CallFunction(g_error, "is", status, what);
+  if (e != nullptr) {
+    PyErr_SetObject(g_error, e);
+    Py_DECREF(e);
+  }
+}
+
+// Product of sizes that no tensor has when it passes 64 bits.
+template <typename... Sizes>
+int64_t product(int64_t first, Sizes... more) {
+  int64_t p = first;
+  if ((__builtin_mul_overflow(p, (int64_t)more, &p) || ...)) return INT64_MAX;
+  return p;
+}
+
+// An entry point's argument names, in order; the last `optional` may be left out (None).
+struct Names {
+  const char* call;
+  int count, optional;
+  const char* const* names;
+};
+constexpr int kMostArgs = 30;
+
 // The arguments of one call, taken in order.
 class Args {
  public:
-  Args(const char* name, PyObject* const* a, Py_ssize_t n, Py_ssize_t want) : name_(name), a_(a) {
-    if (n != want) {
-      PyErr_Format(PyExc_TypeError, "%s: %zd arguments given, %zd wanted", name, n, want);
+  Args(const Names& n, PyObject* const* a, Py_ssize_t given, PyObject* kwnames) : name_(n.call) {
+    if (given > n.count) {
+      PyErr_Format(PyExc_TypeError, "%s: %zd arguments given, %d wanted", name_, given, n.count);
       throw Failed{};
     }
+    for (int i = 0; i < n.count; ++i) a_[i] = i < given ? a[i] : nullptr;
+    const Py_ssize_t named = kwnames == nullptr ? 0 : PyTuple_GET_SIZE(kwnames);
+    for (Py_ssize_t k = 0; k < named; ++k) {
+      PyObject* key = PyTuple_GET_ITEM(kwnames, k);
+      int i = 0;
+      while (i < n.count && PyUnicode_CompareWithASCIIString(key, n.names[i]) != 0) ++i;
+      if (i == n.count || a_[i] != nullptr) {
+        PyErr_Format(PyExc_TypeError, i == n.count ? "%s: no argument %U" : "%s: argument %U given twice", name_, key);
+        throw Failed{};
+      }
+      a_[i] = a[given + k];
+    }
+    for (int i = 0; i < n.count; ++i)
+      if (a_[i] == nullptr) {
+        if (i < n.count - n.optional) {
+          PyErr_Format(PyExc_TypeError, "%s: argument %s is missing", name_, n.names[i]);
+          throw Failed{};
+        }
+        a_[i] = Py_None;
+      }
   }
 
   int64_t i64() {
@@ -49,20 +94,37 @@ class Args {
     if (v == -1 && PyErr_Occurred()) throw Failed{};
     return v;
   }
-  int i32() {
-    const int64_t v = i64();
-    if (v != (int)v) {
-      PyErr_Format(PyExc_OverflowError, "%s: %lld does not fit an int", name_, (long long)v);
-      throw Failed{};
-    }
-    return (int)v;
-  }
+  int i32() { return number32(next()); }
   float f32() {
     const double v = PyFloat_AsDouble(next());
     if (v == -1.0 && PyErr_Occurred()) throw Failed{};
     return (float)v;
   }
   PyObject* object() { return next(); }
+  PyObject* at(int i) { return a_[i]; }
+  bool flag() {
+    PyObject* o = next();
+    if (o == Py_None) return false;
+    const long v = PyLong_AsLong(o);
+    if (v == -1 && PyErr_Occurred()) throw Failed{};
+    if (v != 0 && v != 1) bad_flag_ = true;
+    return v != 0;
+  }
+  bool bad_flag() const { return bad_flag_; }
+
+  // A quantizer spec: an lkv_qspec or (k_bits, v_bits, group).
+  lkv_qspec spec() {
+    PyObject* o = next();
+    lkv_qspec q;
+    if ((PyTuple_Check(o) || PyList_Check(o)) && PySequence_Fast_GET_SIZE(o) == 3) {
+      q.k_bits = number32(PySequence_Fast_GET_ITEM(o, 0));
+      q.v_bits = number32(PySequence_Fast_GET_ITEM(o, 1));
+      q.group = number32(PySequence_Fast_GET_ITEM(o, 2));
+    } else {
+      read(o, &q, sizeof q);
+    }
+    return q;
+  }
 
   // A ctypes structure, by value.
   template <typename T>
@@ -85,8 +147,8 @@ class Args {
   }
 
   // bf16 [n][heads][D] rows whose heads lie side by side; stride: elements from token to token.
-  void* rows(int64_t n, int64_t heads, int64_t D, int64_t& stride) {
-    PyObject *o = next(), *s = next();
+  void* rows(PyObject* s, int64_t n, int64_t heads, int64_t D, int64_t& stride) {
+    PyObject* o = next();
     stride = heads * D;
     if (o == Py_None || PyLong_Check(o)) {
       if (s != Py_None) {
@@ -114,11 +176,15 @@ class Args {
     float* vsz;
   };
   Cache cache(lkv_qspec spec, int64_t rows, int64_t D) {
-    const int64_t pairs = spec.group > 0 ? rows * (D / spec.group) * 2 : 0;
+    const auto bytes = [&](int bits) {
+      const int64_t all = product(rows, D, bits);
+      return all == INT64_MAX ? all : all / 8;
+    };
+    const int64_t pairs = spec.group > 0 ? product(rows, D / spec.group, 2) : 0;
     Cache c{};
-    c.kc = ptr(at::kByte, rows * D * spec.k_bits / 8);
+    c.kc = ptr(at::kByte, bytes(spec.k_bits));
     c.ksz = spec.k_bits == 16 ? (next(), nullptr) : ptr<float>(at::kFloat, pairs);
-    c.vc = ptr(at::kByte, rows * D * spec.v_bits / 8);
+    c.vc = ptr(at::kByte, bytes(spec.v_bits));
     c.vsz = spec.v_bits == 16 ? (next(), nullptr) : ptr<float>(at::kFloat, pairs);
     return c;
   }
@@ -162,6 +228,16 @@ class Args {
   }
 
  private:
+  int number32(PyObject* o) {
+    const long long v = PyLong_AsLongLong(o);
+    if (v == -1 && PyErr_Occurred()) throw Failed{};
+    if (v != (int)v) {
+      PyErr_Format(PyExc_OverflowError, "%s: %lld does not fit an int", name_, v);
+      throw Failed{};
+    }
+    return (int)v;
+  }
+
   static void* number(PyObject* o) {
     void* p = PyLong_AsVoidPtr(o);
     if (p == nullptr && PyErr_Occurred()) throw Failed{};
@@ -202,29 +278,28 @@ class Args {
     s += "] with strides [";
     for (int64_t d = 0; d < t.dim(); ++d) s += (d ? ", " : "") + std::to_string(t.stride(d));
     s += "] on " + t.device().str();
-    PyObject* e = PyObject_CallFunction(g_error, "is", (int)LKV_ERR_INVALID_ARG, s.c_str());
-    if (e != nullptr) {
-      PyErr_SetObject(g_error, e);
-      Py_DECREF(e);
-    }
+    raise(LKV_ERR_INVALID_ARG, s.c_str());
     throw Failed{};
   }
 
   const char* name_;
-  PyObject* const* a_;
-  Py_ssize_t i_ = 0;
-  int dev_ = -1;
+  PyObject* a_[kMostArgs];  // borrowed for the call
+  int i_ = 0, dev_ = -1;
+  bool bad_flag_ = false;
 };
 
 // Runs f, which returns an lkv_status; no C++ exception leaves.
 template <typename F>
-PyObject* guarded(F f) {
+PyObject* guarded(const Names& n, PyObject* const* args, Py_ssize_t given, PyObject* kwnames, F f) {
   try {
     if (g_error == nullptr) {
       PyErr_SetString(PyExc_RuntimeError, "_native is not connected to liblkv.so");
       return nullptr;
     }
-    return PyLong_FromLong(f());
+    Args a(n, args, given, kwnames);
+    const int status = f(a);
+    if (status == LKV_OK) Py_RETURN_NONE;
+    raise(status, n.call);
   } catch (const Failed&) {
   } catch (const std::exception& e) {
     PyErr_SetString(PyExc_RuntimeError, e.what());
@@ -234,9 +309,17 @@ PyObject* guarded(F f) {
   return nullptr;
 }
 
-PyObject* page_plan(PyObject*, PyObject* const* args, Py_ssize_t n) {
-  return guarded([&] {
-    Args a("lkv_page_plan", args, n, 18);
+template <size_t N>
+constexpr Names named(const char* call, int optional, const char* const (&names)[N]) {
+  static_assert(N <= kMostArgs, "room for the arguments");
+  return Names{call, (int)N, optional, names};
+}
+
+constexpr const char* kPlanArgs[] = {"B", "pages_per_seq", "num_pages", "n_cap", "seq_lens", "n_new", "free_pages", "free_cap",
+                                     "free_count", "block_table", "new_lens", "cu_new", "positions", "token_seq", "slots",
+                                     "free_left", "status", "stream"};
+PyObject* page_plan(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject* kw) {
+  return guarded(named("lkv_page_plan", 1, kPlanArgs), args, n, kw, [](Args& a) {
     const int B = a.i32(), pps = a.i32(), pages = a.i32(), cap = a.i32();
     auto* lens = a.ptr<int32_t>(at::kInt, B);
     auto* add = a.ptr<int32_t>(at::kInt, B);
@@ -257,9 +340,9 @@ PyObject* page_plan(PyObject*, PyObject* const* args, Py_ssize_t n) {
   });
 }
 
-PyObject* rope_table(PyObject*, PyObject* const* args, Py_ssize_t n) {
-  return guarded([&] {
-    Args a("lkv_rope_table", args, n, 4);
+constexpr const char* kTableArgs[] = {"spec", "rows", "table", "stream"};
+PyObject* rope_table(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject* kw) {
+  return guarded(named("lkv_rope_table", 1, kTableArgs), args, n, kw, [](Args& a) {
     const auto spec = a.structure<lkv_rope_spec>();
     const int rows = a.i32();
     auto* table = a.ptr<float>(at::kFloat, (int64_t)rows * spec.rot_dim);
@@ -267,18 +350,21 @@ PyObject* rope_table(PyObject*, PyObject* const* args, Py_ssize_t n) {
   });
 }
 
-PyObject* rope_append(PyObject*, PyObject* const* args, Py_ssize_t n) {
-  return guarded([&] {
-    Args a("lkv_rope_append_kv", args, n, 30);
-    const auto spec = a.structure<lkv_qspec>();
+constexpr const char* kAppendArgs[] = {
+    "spec", "n_cap", "Hq", "Hkv", "num_pages", "page_tokens", "D", "n_tokens", "positions", "slots", "q", "k", "v", "q_weight",
+    "k_weight", "eps", "rot_dim", "interleaved", "table", "table_rows", "q_out", "k_codes", "k_sz", "v_codes", "v_sz",
+    "q_stride", "k_stride", "v_stride", "reciprocal", "stream"};
+PyObject* rope_append(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject* kw) {
+  return guarded(named("lkv_rope_append_kv", 5, kAppendArgs), args, n, kw, [](Args& a) {
+    const lkv_qspec spec = a.spec();
     const int cap = a.i32(), Hq = a.i32(), Hkv = a.i32(), pages = a.i32(), page_tokens = a.i32(), D = a.i32();
     auto* n_tokens = a.ptr<int32_t>(at::kInt, 1);
     auto* positions = a.ptr<int32_t>(at::kInt, cap);
     auto* slots = a.ptr<int64_t>(at::kLong, cap);
     int64_t qs, ks, vs;
-    void* q = a.rows(cap, Hq, D, qs);
-    void* k = a.rows(cap, Hkv, D, ks);
-    void* v = a.rows(cap, Hkv, D, vs);
+    void* q = a.rows(a.at(25), cap, Hq, D, qs);
+    void* k = a.rows(a.at(26), cap, Hkv, D, ks);
+    void* v = a.rows(a.at(27), cap, Hkv, D, vs);
     void* wq = a.ptr(at::kBFloat16, D);
     void* wk = a.ptr(at::kBFloat16, D);
     const float eps = a.f32();
@@ -286,52 +372,67 @@ PyObject* rope_append(PyObject*, PyObject* const* args, Py_ssize_t n) {
     PyObject* table_o = a.object();
     const int rows = a.i32();
     auto* table = static_cast<float*>(a.address(table_o, at::kFloat, (int64_t)rows * rot));
-    void* q_out = a.ptr(at::kBFloat16, (int64_t)cap * Hq * D);
-    const auto c = a.cache(spec, (int64_t)pages * Hkv * page_tokens, D);
-    const int reciprocal = a.i32();
+    void* q_out = a.ptr(at::kBFloat16, product(cap, Hq, D));
+    const auto c = a.cache(spec, product(pages, Hkv, page_tokens), D);
+    for (int i = 0; i < 3; ++i) a.object();  // the strides
+    const bool reciprocal = a.flag();
     return g_entry.rope_append(spec, cap, Hq, Hkv, pages, page_tokens, D, n_tokens, positions, slots, q, qs, k, ks, v, vs,
-                               wq, wk, eps, rot, inter, table, rows, q_out, c.kc, c.ksz, c.vc, c.vsz, reciprocal, a.stream());
+                               wq, wk, eps, rot, inter, table, rows, q_out, c.kc, c.ksz, c.vc, c.vsz,
+                               a.bad_flag() ? 2 : reciprocal, a.stream());
   });
 }
 
-PyObject* multi(PyObject*, PyObject* const* args, Py_ssize_t n) {
-  return guarded([&] {
-    Args a("lkv_decode_attention_multi", args, n, 21);
-    const auto spec = a.structure<lkv_qspec>();
+// What both forms of the attention take behind the cache.
+struct Tail {
+  lkv_score_rule rule;
+  float *out, *lse;
+  void* ws;
+  int64_t bytes;
+  void* stream;
+};
+Tail tail(Args& a, int64_t Hq, int64_t B, int64_t rows, int64_t D) {
+  Tail t;
+  t.rule = a.rule(Hq, B);
+  t.out = a.ptr<float>(at::kFloat, product(rows, Hq, D));
+  t.lse = a.ptr<float>(at::kFloat, rows * Hq);
+  PyObject* ws = a.object();
+  t.bytes = a.i64();
+  t.ws = a.address(ws, at::kByte, t.bytes);
+  t.stream = a.stream();
+  return t;
+}
+
+constexpr const char* kMultiArgs[] = {"spec", "B", "Hq", "Hkv", "T_cap", "D", "max_q", "n_rows", "seq_lens", "cu_q", "q",
+                                      "k_codes", "k_sz", "v_codes", "v_sz", "rule", "out", "lse", "workspace", "ws_bytes", "stream"};
+PyObject* multi(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject* kw) {
+  return guarded(named("lkv_decode_attention_multi", 1, kMultiArgs), args, n, kw, [](Args& a) {
+    const lkv_qspec spec = a.spec();
     const int B = a.i32(), Hq = a.i32(), Hkv = a.i32(), T = a.i32(), D = a.i32(), max_q = a.i32(), rows = a.i32();
     auto* lens = a.ptr<int32_t>(at::kInt, B);
     auto* cu = a.ptr<int32_t>(at::kInt, (int64_t)B + 1);
-    void* q = a.ptr(at::kBFloat16, (int64_t)rows * Hq * D);
-    const auto c = a.cache(spec, (int64_t)B * Hkv * T, D);
-    const auto rule = a.rule(Hq, B);
-    auto* out = a.ptr<float>(at::kFloat, (int64_t)rows * Hq * D);
-    auto* lse = a.ptr<float>(at::kFloat, (int64_t)rows * Hq);
-    PyObject* ws_o = a.object();
-    const int64_t bytes = a.i64();
-    void* ws = a.address(ws_o, at::kByte, bytes);
-    return g_entry.multi(spec, B, Hq, Hkv, T, D, max_q, rows, lens, cu, q, c.kc, c.ksz, c.vc, c.vsz, rule, out, lse, ws,
-                         (size_t)bytes, a.stream());
+    void* q = a.ptr(at::kBFloat16, product(rows, Hq, D));
+    const auto c = a.cache(spec, product(B, Hkv, T), D);
+    const Tail t = tail(a, Hq, B, rows, D);
+    return g_entry.multi(spec, B, Hq, Hkv, T, D, max_q, rows, lens, cu, q, c.kc, c.ksz, c.vc, c.vsz, t.rule, t.out, t.lse, t.ws,
+                         (size_t)t.bytes, t.stream);
   });
 }
 
-PyObject* multi_paged(PyObject*, PyObject* const* args, Py_ssize_t n) {
-  return guarded([&] {
-    Args a("lkv_decode_attention_multi_paged", args, n, 23);
-    const auto spec = a.structure<lkv_qspec>();
+constexpr const char* kPagedArgs[] = {"spec", "B", "Hq", "Hkv", "pages_per_seq", "num_pages", "D", "max_q", "n_rows", "seq_lens",
+                                      "cu_q", "q", "block_table", "k_pool", "k_sz_pool", "v_pool", "v_sz_pool", "rule", "out",
+                                      "lse", "workspace", "ws_bytes", "stream"};
+PyObject* multi_paged(PyObject*, PyObject* const* args, Py_ssize_t n, PyObject* kw) {
+  return guarded(named("lkv_decode_attention_multi_paged", 1, kPagedArgs), args, n, kw, [](Args& a) {
+    const lkv_qspec spec = a.spec();
     const int B = a.i32(), Hq = a.i32(), Hkv = a.i32(), pps = a.i32(), pages = a.i32(), D = a.i32(), max_q = a.i32(), rows = a.i32();
     auto* lens = a.ptr<int32_t>(at::kInt, B);
     auto* cu = a.ptr<int32_t>(at::kInt, (int64_t)B + 1);
-    void* q = a.ptr(at::kBFloat16, (int64_t)rows * Hq * D);
+    void* q = a.ptr(at::kBFloat16, product(rows, Hq, D));
     auto* table = a.ptr<int32_t>(at::kInt, (int64_t)B * pps);
-    const auto c = a.cache(spec, (int64_t)pages * Hkv * LKV_PAGE_TOKENS, D);
-    const auto rule = a.rule(Hq, B);
-    auto* out = a.ptr<float>(at::kFloat, (int64_t)rows * Hq * D);
-    auto* lse = a.ptr<float>(at::kFloat, (int64_t)rows * Hq);
-    PyObject* ws_o = a.object();
-    const int64_t bytes = a.i64();
-    void* ws = a.address(ws_o, at::kByte, bytes);
+    const auto c = a.cache(spec, product(pages, Hkv, LKV_PAGE_TOKENS), D);
+    const Tail t = tail(a, Hq, B, rows, D);
     return g_entry.multi_paged(spec, B, Hq, Hkv, pps, pages, D, max_q, rows, lens, cu, q, table, c.kc, c.ksz, c.vc, c.vsz,
-                               rule, out, lse, ws, (size_t)bytes, a.stream());
+                               t.rule, t.out, t.lse, t.ws, (size_t)t.bytes, t.stream);
   });
 }
 
@@ -348,14 +449,24 @@ PyObject* connect(PyObject*, PyObject* args) {
   Py_RETURN_NONE;
 }
 
-#define FAST(f) reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL
+#define FAST(f) reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL | METH_KEYWORDS
 PyMethodDef g_methods[] = {
     {"connect", connect, METH_VARARGS, "connect(LkvError, addresses of the entry points)"},
-    {"lkv_page_plan", FAST(page_plan), nullptr},
-    {"lkv_rope_table", FAST(rope_table), nullptr},
-    {"lkv_rope_append_kv", FAST(rope_append), nullptr},
-    {"lkv_decode_attention_multi", FAST(multi), nullptr},
-    {"lkv_decode_attention_multi_paged", FAST(multi_paged), nullptr},
+    {"lkv_page_plan", FAST(page_plan),
+     "lkv_page_plan(B, pages_per_seq, num_pages, n_cap, seq_lens, n_new, free_pages, free_cap, free_count, block_table, new_lens, "
+     "cu_new, positions, token_seq, slots, free_left, status, stream=None)\n--\n\nThe call of include/lkv.h."},
+    {"lkv_rope_table", FAST(rope_table), "lkv_rope_table(spec, rows, table, stream=None)\n--\n\nThe call of include/lkv.h."},
+    {"lkv_rope_append_kv", FAST(rope_append),
+     "lkv_rope_append_kv(spec, n_cap, Hq, Hkv, num_pages, page_tokens, D, n_tokens, positions, slots, q, k, v, q_weight, k_weight, "
+     "eps, rot_dim, interleaved, table, table_rows, q_out, k_codes, k_sz, v_codes, v_sz, q_stride=None, k_stride=None, "
+     "v_stride=None, reciprocal=None, stream=None)\n--\n\nThe call of include/lkv.h.  q, k, v: bf16 [n_cap][heads][D], views of a fused "
+     "projection among them (the strides are for integer addresses only)."},
+    {"lkv_decode_attention_multi", FAST(multi),
+     "lkv_decode_attention_multi(spec, B, Hq, Hkv, T_cap, D, max_q, n_rows, seq_lens, cu_q, q, k_codes, k_sz, v_codes, v_sz, rule, "
+     "out, lse, workspace, ws_bytes, stream=None)\n--\n\nThe call of include/lkv.h."},
+    {"lkv_decode_attention_multi_paged", FAST(multi_paged),
+     "lkv_decode_attention_multi_paged(spec, B, Hq, Hkv, pages_per_seq, num_pages, D, max_q, n_rows, seq_lens, cu_q, q, block_table, "
+     "k_pool, k_sz_pool, v_pool, v_sz_pool, rule, out, lse, workspace, ws_bytes, stream=None)\n--\n\nThe call of include/lkv.h."},
     {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_native", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};

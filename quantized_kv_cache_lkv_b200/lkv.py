@@ -312,11 +312,14 @@ def lkv_tiered_decode(B, Hq, Hkv, T_cap, D, group, seq_lens, mass, tau_low, tau_
 # passed on, at a tenth of what the same checks cost here.  Integer addresses go
 # through unchecked.
 
+_NATIVE = ("lkv_page_plan", "lkv_rope_table", "lkv_rope_append_kv", "lkv_decode_attention_multi",
+           "lkv_decode_attention_multi_paged")
 _nat = None
 
 
 def native():
-    """The native module, connected to liblkv.so (raises if either has not been built)."""
+    """The native module, connected to liblkv.so (raises if either has not been built).  Its functions then stand
+    here under their names."""
     global _nat
     if _nat is None:
         import torch  # noqa: F401  (its libraries come before the module's)
@@ -326,60 +329,42 @@ def native():
             raise RuntimeError("the _native module is missing: build it with "
                                "`python -m quantized_kv_cache_lkv_b200.build`") from e
         L = lib()
-        _native.connect(LkvError, *(ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in (
-            "lkv_page_plan", "lkv_rope_table", "lkv_rope_append_kv", "lkv_decode_attention_multi",
-            "lkv_decode_attention_multi_paged")))
+        _native.connect(LkvError, *(ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in _NATIVE))
+        globals().update({n: getattr(_native, n) for n in _NATIVE})
         _nat = _native
     return _nat
 
 
-def lkv_page_plan(B, pages_per_seq, num_pages, n_cap, seq_lens, n_new, free_pages, free_cap, free_count, block_table,
-                  new_lens, cu_new, positions, token_seq, slots, free_left, status, stream=None):
-    rc = (_nat or native()).lkv_page_plan(B, pages_per_seq, num_pages, n_cap, seq_lens, n_new, free_pages, free_cap,
-                                          free_count, block_table, new_lens, cu_new, positions, token_seq, slots,
-                                          free_left, status, stream)
-    if rc:
-        raise LkvError(rc, "lkv_page_plan")
+def lkv_page_plan(*args, **kwargs):
+    """(B, pages_per_seq, num_pages, n_cap, seq_lens, n_new, free_pages, free_cap, free_count, block_table, new_lens,
+    cu_new, positions, token_seq, slots, free_left, status, stream=None)"""
+    return native().lkv_page_plan(*args, **kwargs)
 
 
-def lkv_rope_table(spec, rows, table, stream=None):
-    rc = (_nat or native()).lkv_rope_table(spec, rows, table, stream)
-    if rc:
-        raise LkvError(rc, "lkv_rope_table")
+def lkv_rope_table(*args, **kwargs):
+    """(spec, rows, table, stream=None)"""
+    return native().lkv_rope_table(*args, **kwargs)
 
 
-def lkv_rope_append_kv(spec, n_cap, Hq, Hkv, num_pages, page_tokens, D, n_tokens, positions, slots, q, k, v, q_weight,
-                       k_weight, eps, rot_dim, interleaved, table, table_rows, q_out, k_codes, k_sz, v_codes, v_sz,
-                       q_stride=None, k_stride=None, v_stride=None, reciprocal=False, stream=None):
-    """q, k, v: bf16 [n_cap][heads][D], views of a fused projection among them (the strides are for integer
-    addresses only)."""
-    rc = (_nat or native()).lkv_rope_append_kv(_spec(spec), n_cap, Hq, Hkv, num_pages, page_tokens, D, n_tokens,
-                                               positions, slots, q, q_stride, k, k_stride, v, v_stride, q_weight,
-                                               k_weight, eps, rot_dim, interleaved, table, table_rows, q_out, k_codes,
-                                               k_sz, v_codes, v_sz, reciprocal, stream)
-    if rc:
-        raise LkvError(rc, "lkv_rope_append_kv")
+def lkv_rope_append_kv(*args, **kwargs):
+    """(spec, n_cap, Hq, Hkv, num_pages, page_tokens, D, n_tokens, positions, slots, q, k, v, q_weight, k_weight, eps,
+    rot_dim, interleaved, table, table_rows, q_out, k_codes, k_sz, v_codes, v_sz, q_stride=None, k_stride=None,
+    v_stride=None, reciprocal=False, stream=None); q, k, v: bf16 [n_cap][heads][D], views of a fused projection among
+    them (the strides are for integer addresses only)"""
+    return native().lkv_rope_append_kv(*args, **kwargs)
 
 
 def lkv_multi_workspace_bytes(spec, B, Hq, Hkv, T_cap, D, max_q):
     return lib().lkv_multi_workspace_bytes(_spec(spec), B, Hq, Hkv, T_cap, D, max_q)
 
 
-def lkv_decode_attention_multi(spec, B, Hq, Hkv, T_cap, D, max_q, n_rows, seq_lens, cu_q, q, k_codes, k_sz, v_codes,
-                               v_sz, rule, out, lse, workspace, ws_bytes, stream=None):
-    rc = (_nat or native()).lkv_decode_attention_multi(_spec(spec), B, Hq, Hkv, T_cap, D, max_q, n_rows, seq_lens, cu_q,
-                                                       q, k_codes, k_sz, v_codes, v_sz, rule, out, lse, workspace,
-                                                       ws_bytes, stream)
-    if rc:
-        raise LkvError(rc, "lkv_decode_attention_multi")
+def lkv_decode_attention_multi(*args, **kwargs):
+    """(spec, B, Hq, Hkv, T_cap, D, max_q, n_rows, seq_lens, cu_q, q, k_codes, k_sz, v_codes, v_sz, rule, out, lse,
+    workspace, ws_bytes, stream=None)"""
+    return native().lkv_decode_attention_multi(*args, **kwargs)
 
 
-def lkv_decode_attention_multi_paged(spec, B, Hq, Hkv, pages_per_seq, num_pages, D, max_q, n_rows, seq_lens, cu_q, q,
-                                     block_table, k_pool, k_sz_pool, v_pool, v_sz_pool, rule, out, lse, workspace,
-                                     ws_bytes, stream=None):
-    rc = (_nat or native()).lkv_decode_attention_multi_paged(_spec(spec), B, Hq, Hkv, pages_per_seq, num_pages, D, max_q,
-                                                             n_rows, seq_lens, cu_q, q, block_table, k_pool, k_sz_pool,
-                                                             v_pool, v_sz_pool, rule, out, lse, workspace, ws_bytes,
-                                                             stream)
-    if rc:
-        raise LkvError(rc, "lkv_decode_attention_multi_paged")
+def lkv_decode_attention_multi_paged(*args, **kwargs):
+    """(spec, B, Hq, Hkv, pages_per_seq, num_pages, D, max_q, n_rows, seq_lens, cu_q, q, block_table, k_pool,
+    k_sz_pool, v_pool, v_sz_pool, rule, out, lse, workspace, ws_bytes, stream=None)"""
+    return native().lkv_decode_attention_multi_paged(*args, **kwargs)

@@ -178,3 +178,33 @@ def test_tensors_that_do_not_fit():
         lkv.lkv_decode_attention_multi(**multi_args(rule=None))
     with pytest.raises(OverflowError):
         lkv.lkv_page_plan(**plan_args(B=1 << 40))
+
+
+def test_arguments_by_position_and_name():
+    """Both reach the same call; a name that is unknown, given twice or missing is refused."""
+    ok = lkv.lkv_rope_spec()
+    assert rc_of(lkv.lkv_rope_table, stream=0, table=FAKE + 8, rows=1, spec=ok) == ARG
+    with pytest.raises(lkv.LkvError) as e:
+        lkv.lkv_rope_table(ok, 1, FAKE + 8, stream=0)
+    assert e.value.status == ARG
+    assert lkv.lkv_rope_table(ok, 0, None, 0) is None
+    for args, kw in (((ok, 0, None, 0, 0), {}), ((ok, 0), {}), ((ok, 0, None), dict(row=1)), ((ok, 0, None), dict(rows=1)), ((), {})):
+        with pytest.raises(TypeError):
+            lkv.lkv_rope_table(*args, **kw)
+
+
+@pytest.mark.parametrize("spec,want", [((6, 4, 64), 0), ([6, 4, 64], 0), (lkv.lkv_qspec(6, 4, 64), 0), ((5, 4, 64), lkv.LKV_ERR_UNSUPPORTED)])
+def test_spec_forms(spec, want):
+    assert rc_of(lkv.lkv_decode_attention_multi, **multi_args(spec=spec, n_rows=0, q=None, out=None)) == want
+
+
+@pytest.mark.parametrize("spec", [(6, 4), None, "k6v4", (6, 4, "64"), lkv.lkv_rope_spec()])
+def test_specs_refused(spec):
+    with pytest.raises(TypeError):
+        lkv.lkv_decode_attention_multi(**multi_args(spec=spec))
+
+
+@pytest.mark.parametrize("flag,want", [(None, 0), (False, 0), (True, 0), (0, 0), (1, 0), (2, ARG), (-1, ARG)])
+def test_reciprocal_is_a_flag(flag, want):
+    assert rc_of(lkv.lkv_rope_append_kv, **append_args(n_cap=0, q=None, k=None, v=None, q_out=None, slots=None, positions=None,
+                                                       reciprocal=flag)) == want

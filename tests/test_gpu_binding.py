@@ -57,3 +57,18 @@ def test_streams():
             table(t, stream=given)
         s.synchronize()
         assert torch.equal(t, want)
+
+
+def test_sizes_past_64_bits():
+    """No tensor has room for a pool whose size passes 64 bits, whatever the product's low bits are."""
+    c = [torch.zeros(1, 4, 256, 96, dtype=torch.uint8, device="cuda"), torch.zeros(1, 4, 256, 2, 2, device="cuda"),
+         torch.zeros(1, 4, 256, 64, dtype=torch.uint8, device="cuda"), torch.zeros(1, 4, 256, 2, 2, device="cuda")]
+
+    def call(pages, heads):  # no tokens: nothing is launched
+        lkv.lkv_rope_append_kv((6, 4, 64), 0, heads, heads, pages, 256, 128, None, None, None, None, None, None, None, None, 0.0,
+                               0, False, None, 0, None, *c)
+
+    call(1, 4)
+    with pytest.raises(lkv.LkvError) as e:
+        call(1 << 30, 1 << 20)
+    assert e.value.status == lkv.LKV_ERR_INVALID_ARG
