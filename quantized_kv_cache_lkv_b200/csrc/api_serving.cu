@@ -47,6 +47,9 @@ int multi_impl(lkv_qspec spec, int B, int Hq, int Hkv, int T_cap, int D, int max
     return LKV_ERR_INVALID_ARG;
   // scores are divided by the cap: a smaller one takes them out of fp32
   if (rule.softcap > 0.0f && rule.softcap < 1e-30f) return LKV_ERR_INVALID_ARG;
+  // the factor of q . khat; an infinite one would make NaN of a product that is 0
+  if (!std::isfinite(rule.softcap > 0.0f ? rule.softmax_scale / rule.softcap : rule.softmax_scale * 1.442695f))
+    return LKV_ERR_INVALID_ARG;
   if (!int_ptr_ok(rule.slopes, false) || !int_ptr_ok(rule.prefix_lens, false) || !int_ptr_ok(rule.doc_starts, false) ||
       !int_ptr_ok(cu_q, false) || !int_ptr_ok(lse, false) || !int_ptr_ok(seq_lens, B > 0))
     return LKV_ERR_INVALID_ARG;

@@ -208,3 +208,9 @@ def test_specs_refused(spec):
 def test_reciprocal_is_a_flag(flag, want):
     assert rc_of(lkv.lkv_rope_append_kv, **append_args(n_cap=0, q=None, k=None, v=None, q_out=None, slots=None, positions=None,
                                                        reciprocal=flag)) == want
+
+
+@pytest.mark.parametrize("scale,cap,want", [(1e38, 1e-3, ARG), (-1e38, 1e-3, ARG), (3e38, 0.0, ARG), (3e38, 50.0, 0), (2e38, 0.0, 0),
+                                            (1e-38, 1e-30, 0)])
+def test_score_factor_is_finite(scale, cap, want):
+    assert rc_of(lkv.lkv_decode_attention_multi, **multi_args(rule=rule(softmax_scale=scale, softcap=cap), n_rows=0, q=None, out=None)) == want
