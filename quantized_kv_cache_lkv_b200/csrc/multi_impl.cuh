@@ -45,8 +45,8 @@
 // in order, so results do not depend on timing.
 //
 // Measured on a B200, device time: K6V4, B16 x 8192, 32 / 8 heads, capped and
-// paged: 75 us for 201.7 MB (2.7 TB/s); 16 query rows over 131072 tokens: 115 us;
-// 8-bit, G 32, 64 ragged sequences behind a window of 1024: 60 us for 167 MB.
+// paged: 74 us for 201.7 MB (2.7 TB/s); 16 query rows over 131072 tokens: 114 us;
+// 8-bit, G 32, 64 ragged sequences behind a window of 1024: 58 us for 167 MB.
 // 1030 instructions a tile of 32 tokens, half of the issue slots used.
 #pragma once
 #include <type_traits>
@@ -995,7 +995,7 @@ constexpr int kFresh = 1 << 8, kEnd = 1 << 9;
 // Start the copies of a tile into a stage, one lane each; the bytes complete on bar.
 template <typename C>
 __device__ __forceinline__ void fetch_tile(const MultiArgs& a, Feed& f, uint8_t* stage, int4* what, uint64_t* bar,
-                                           const uint8_t* src, int row_bytes, int off, uint64_t policy) {
+                                           const uint8_t* src, int row_bytes, int off) {
   const int lane = threadIdx.x & 31;
   int n = max(0, min(C::TT, f.T - f.t0));
   if (lane == 0) *what = make_int4(f.t0, n | (f.fresh ? kFresh : 0) | (f.left == 1 ? kEnd : 0), f.b, f.ui);
@@ -1018,7 +1018,7 @@ __device__ __forceinline__ void fetch_tile(const MultiArgs& a, Feed& f, uint8_t*
     constexpr int all = C::KRB + C::VRB + (C::KB < 16 ? C::NG * 8 : 0) + (C::VB < 16 ? C::NG * 8 : 0);
     if (lane == 0) mbar_arrive_expect_tx(bar, n * all);
     __syncwarp();
-    if (lane < 4 && row_bytes > 0) bulk_g2s(stage + off, src + row * row_bytes, n * row_bytes, bar, policy);
+    if (lane < 4 && row_bytes > 0) bulk_g2s(stage + off, src + row * row_bytes, n * row_bytes, bar, policy_evict_first());
   }
 }
 
@@ -1031,60 +1031,52 @@ __device__ __forceinline__ T ld(const T* p) {
   else return *p;
 }
 
-// By one warp: the row's reference and sum, and its weights
-// (wt[(k - p0) * 8 NT + row]); a piece per lane and step.
+// Row `row` of the pieces p0 .. p1 - 1 joined (at(k) is where piece k lies), by
+// any number of threads on their own: the row's reference and sum, and four
+// channels (the i-th float4 of a piece's output).  Eight pieces are in flight
+// at a time, their references and sums with them: every thread of a row makes
+// the weights 2^(ref_k - max) again, which costs less than a first pass and a
+// barrier (71 us with those, 66 without: 16-bit documents, 16 query rows).
 template <int NT, bool L2, typename At>
-__device__ __forceinline__ float2 join_row(int p0, int p1, const At& at, int row, float* wt) {
-  const int lane = threadIdx.x & 31;
+__device__ __forceinline__ void join_pieces(int p0, int p1, const At& at, int row, int i, float2& ml, float4& o) {
   float m = -INFINITY, l = 0.0f;
-  for (int k0 = p0; k0 < p1; k0 += 32) {
-    const int k = k0 + lane;
-    float2 ml = make_float2(-INFINITY, 0.0f);
-    if (k < p1) ml = ld<L2>(reinterpret_cast<const float2*>(at(k) + 2 * row));
-    float t = ml.x;
-#pragma unroll
-    for (int off = 16; off >= 1; off >>= 1) t = fmaxf(t, __shfl_xor_sync(kFull, t, off));
-    t = fmaxf(t, m);
-    if (k < p1) wt[(k - p0) * 8 * NT + row] = ml.x;  // its reference, until the largest is known
-    l *= m == t ? 1.0f : pow2i(m - t);                   // references are integers: exact
-    float part = ml.x == -INFINITY ? 0.0f : ml.y * pow2i(ml.x - t);
-#pragma unroll
-    for (int off = 16; off >= 1; off >>= 1) part += __shfl_xor_sync(kFull, part, off);
-    l += part;
-    m = t;
-  }
-  __syncwarp();
-  for (int k = p0 + lane; k < p1; k += 32) {
-    float& x = wt[(k - p0) * 8 * NT + row];
-    x = x == -INFINITY ? 0.0f : pow2i(x - m);
-  }
-  return make_float2(m, l);
-}
-
-// Four channels of the joined output: eight pieces in flight at a time.
-template <int NT, bool L2, typename At>
-__device__ __forceinline__ float4 join_out(int p0, int p1, const At& at, int row, int i, const float* wt) {
-  float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   for (int k0 = p0; k0 < p1; k0 += 8) {
+    float2 w[8];
     float4 v[8];
-    float f[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const int k = k0 + j;
+      w[j] = make_float2(-INFINITY, 0.0f);
       v[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-      f[j] = 0.0f;
-      if (k < p1) {
-        v[j] = ld<L2>(reinterpret_cast<const float4*>(at(k) + 16 * NT) + i);
-        f[j] = wt[(k - p0) * 8 * NT + row];
+      if (k0 + j < p1) {
+        const float* p = at(k0 + j);
+        w[j] = ld<L2>(reinterpret_cast<const float2*>(p) + row);
+        v[j] = ld<L2>(reinterpret_cast<const float4*>(p + 16 * NT) + i);
       }
     }
+    float t = m;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) t = fmaxf(t, w[j].x);
+    const float back = m == t ? 1.0f : pow2i(m - t);  // references are integers: exact
+    l *= back;
+    o.x *= back; o.y *= back; o.z *= back; o.w *= back;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      o.x = fmaf(v[j].x, f[j], o.x); o.y = fmaf(v[j].y, f[j], o.y);
-      o.z = fmaf(v[j].z, f[j], o.z); o.w = fmaf(v[j].w, f[j], o.w);
+      const float f = w[j].x == -INFINITY ? 0.0f : pow2i(w[j].x - t);
+      l = fmaf(w[j].y, f, l);
+      o.x = fmaf(v[j].x, f, o.x); o.y = fmaf(v[j].y, f, o.y);
+      o.z = fmaf(v[j].z, f, o.z); o.w = fmaf(v[j].w, f, o.w);
     }
+    m = t;
   }
-  return o;
+  ml = make_float2(m, l);
+}
+
+// Publishes what the block wrote before its barrier, and shows what other blocks published before.
+__device__ __forceinline__ int add_acq_rel(int* p, int x) {
+  int old;
+  asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], %2;" : "=r"(old) : "l"(p), "r"(x) : "memory");
+  return old;
 }
 
 template <typename C>
@@ -1204,7 +1196,6 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) multi_kernel(MultiArgs a) {
     const int w0 = warp_begin(warp), w1 = warp_begin(warp + 1);
     if (w0 < w1) {
       const uint64_t limit = *a.timeout_ns ? *a.timeout_ns : 2000000000ull;
-      const uint64_t policy = policy_evict_first();
       // lanes 0 .. 3 copy K codes, K pairs, V codes, V pairs
       const uint8_t* src = lane == 0 ? a.kc : lane == 1 ? reinterpret_cast<const uint8_t*>(a.ksz)
                            : lane == 2 ? a.vc : reinterpret_cast<const uint8_t*>(a.vsz);
@@ -1218,7 +1209,7 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) multi_kernel(MultiArgs a) {
       int fx = w0;
       for (int i = 0; i < ST && fx < w1; ++i, ++fx) {
         if (i > 0) feed_next<NT, TT>(a, first, f);
-        fetch_tile<C>(a, f, ring + i * C::STAGE, what + i, bar + i, src, row_bytes, off, policy);
+        fetch_tile<C>(a, f, ring + i * C::STAGE, what + i, bar + i, src, row_bytes, off);
       }
       __syncwarp();
       if (warp == W - 1) find_cuts();
@@ -1246,7 +1237,7 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) multi_kernel(MultiArgs a) {
         __syncwarp();
         if (fx < w1 && !dead) {
           feed_next<NT, TT>(a, first, f);
-          fetch_tile<C>(a, f, stage, what + st, bar + st, src, row_bytes, off, policy);
+          fetch_tile<C>(a, f, stage, what + st, bar + st, src, row_bytes, off);
           ++fx;
         }
         st = st + 1 == ST ? 0 : st + 1;
@@ -1268,16 +1259,11 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) multi_kernel(MultiArgs a) {
     }
   }
   __syncthreads();
-
-  __syncthreads();
   const int ncut = s_ncut;
   if (ncut == 0) return;
+  const int b0 = s_begin[0], b1 = s_begin[W];  // x0 and x1: not kept in registers across the loop, which has none to spare
   constexpr int ROWS = 8 * NT, EL = ROWS * D / 4;
-  // in the scratch of the warps; the rings hold pieces
-  float2* s_ml = reinterpret_cast<float2*>(smem + W * ST * C::STAGE);  // [cuts][ROWS]
-  float* s_wt = reinterpret_cast<float*>(s_ml + (W + 1) * ROWS);       // [cut + piece][ROWS]
-  static_assert(((W + 1) * 2 + 2 * W + 1) * ROWS * 4 <= W * C::SCRATCH, "sums and weights fit the scratch");
-  auto is_shared = [&](const Cut& u) { return u.u0 < x0 || u.u1 > x1; };
+  auto is_shared = [&](const Cut& u) { return u.u0 < b0 || u.u1 > b1; };
   auto out_row = [&](const Cut& u, int row) {
     const int i = (u.row0 + row) / a.r;
     return (long long)(u.c0 + i) * a.Hq + u.g * a.r + (u.row0 + row) - i * a.r;
@@ -1295,24 +1281,21 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) multi_kernel(MultiArgs a) {
     return reinterpret_cast<const float*>(smem + (size_t)k * ST * C::STAGE);
   };
   float* const to0 = a.cpieces + (long long)2 * cta * PF;
-  for (int i = warp; i < ncut * ROWS; i += W) {
-    const Cut& u = s_cut[i / ROWS];
-    const int row = i % ROWS;
-    if (row >= u.rows) continue;
-    const float2 ml = join_row<NT, false>(u.k0, u.k1, [&](int k) { return piece_of(u, k); }, row, s_wt + (u.k0 + i / ROWS) * ROWS);
-    if (lane != 0) continue;
-    s_ml[i] = ml;
-    if (is_shared(u)) *reinterpret_cast<float2*>(to0 + (u.u0 > x0 ? PF : 0) + 2 * row) = ml;
-    else write_row(u, row, ml);
-  }
-  __syncthreads();
   for (int el = tid; el < ncut * EL; el += 32 * W) {
     const int i = el / EL, at = el % EL, row = at / (D / 4);
     const Cut& u = s_cut[i];
     if (row >= u.rows) continue;
-    const float4 o = join_out<NT, false>(u.k0, u.k1, [&](int k) { return piece_of(u, k); }, row, at, s_wt + (u.k0 + i) * ROWS);
-    if (is_shared(u)) reinterpret_cast<float4*>(to0 + (u.u0 > x0 ? PF : 0) + 16 * NT)[at] = o;
-    else write_out(u, row, at % (D / 4), s_ml[i * ROWS + row], o);
+    float2 ml;
+    float4 o;
+    join_pieces<NT, false>(u.k0, u.k1, [&](int k) { return piece_of(u, k); }, row, at, ml, o);
+    float* const to = to0 + (u.u0 > b0 ? PF : 0);
+    if (is_shared(u)) {
+      if (at % (D / 4) == 0) reinterpret_cast<float2*>(to)[row] = ml;
+      reinterpret_cast<float4*>(to + 16 * NT)[at] = o;
+    } else {
+      if (at % (D / 4) == 0) write_row(u, row, ml);
+      write_out(u, row, at % (D / 4), ml, o);
+    }
   }
   // a unit that began in an earlier CTA can only be the first, one that ends in a later the last
   if (!is_shared(s_cut[0]) && !is_shared(s_cut[ncut - 1])) return;
@@ -1323,31 +1306,26 @@ __global__ void __launch_bounds__(32 * C::WARPS, 1) multi_kernel(MultiArgs a) {
     const int i = tid == 0 ? 0 : ncut - 1;
     const Cut& u = s_cut[i];
     if (is_shared(u) && (tid == 0 || i != 0)) {
-      __threadfence();
       int* arrive = a.arrive + u.ck0;  // a CTA begins at most one unit that it does not end
-      if (atomicAdd(arrive, 1) + 1 == u.ck1 - u.ck0) {
+      if (add_acq_rel(arrive, 1) + 1 == u.ck1 - u.ck0) {
         *arrive = 0;  // ready for the next call
-        __threadfence();
         s_last[tid] = 1;
       }
     }
   }
   __syncthreads();
-  s_wt = reinterpret_cast<float*>(smem);  // the rings are done with
   for (int t = 0; t < 2; ++t) {
     if (!s_last[t]) continue;  // the same for every thread
     const Cut& u = s_cut[t == 0 ? 0 : ncut - 1];
     auto at = [&](int k) -> const float* { return a.cpieces + (long long)(2 * k + (k == u.ck0 ? u.slot : 0)) * PF; };
-    for (int row = warp; row < u.rows; row += W) {
-      const float2 ml = join_row<NT, true>(u.ck0, u.ck1, at, row, s_wt);
-      if (lane != 0) continue;
-      s_ml[row] = ml;
-      write_row(u, row, ml);
+    for (int i = tid; i < u.rows * (D / 4); i += 32 * W) {
+      const int row = i / (D / 4);
+      float2 ml;
+      float4 o;
+      join_pieces<NT, true>(u.ck0, u.ck1, at, row, i, ml, o);
+      if (i % (D / 4) == 0) write_row(u, row, ml);
+      write_out(u, row, i % (D / 4), ml, o);
     }
-    __syncthreads();
-    for (int i = tid; i < u.rows * (D / 4); i += 32 * W)
-      write_out(u, i / (D / 4), i % (D / 4), s_ml[i / (D / 4)], join_out<NT, true>(u.ck0, u.ck1, at, i / (D / 4), i, s_wt));
-    __syncthreads();
   }
 }
 
