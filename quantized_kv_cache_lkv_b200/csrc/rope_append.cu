@@ -16,9 +16,11 @@
 // registers once per run.  Query rows need no channel order for the output,
 // so in the half layout lane j takes the 8 channels from 8j and the 8 from
 // rot/2 + 8j: whole pairs, no exchange between lanes.  Key rows are quantized
-// in groups of adjacent channels, so there a lane keeps its 16 adjacent ones
-// and reads their partners too (one row in six at 32 / 8 heads).  16384 tokens of
-// 32 / 8 heads into a K6V4 cache: 93 us for 369 MB (4.0 TB/s); 16 tokens: 3.7 us.
+// in groups of adjacent channels: they are rotated like queries and change
+// order through shared memory (16384 tokens: 86 us, and 92 where lanes kept
+// their 16 adjacent channels and read and normed the partners too).  16384
+// tokens of 32 / 8 heads into a K6V4 cache: 85 us for 369 MB (4.3 TB/s); 16
+// tokens: 3.3 us.
 #include <algorithm>
 
 #include "serving.cuh"
@@ -28,8 +30,10 @@ namespace lkv {
 namespace {
 
 constexpr int kWarps = 4;
-constexpr int kBlocksPerSm = 6;  // 80 registers; 5 blocks: 103 us instead of 93 for 16384 tokens of 32 / 8 heads
-constexpr int kRun = 4;          // query batches of a warp in large calls (2: 129 us, 8: 96 us)
+// 72 registers (16384 tokens of 32 / 8 heads: 5 blocks 95 us, 6 86, 7 85, 8 88);
+// where only some channels turn 80 (64 of 128: 6 blocks 95 us, 7 99)
+constexpr int blocks_per_sm(bool whole) { return whole ? 7 : 6; }
+constexpr int kRun = 4;  // query batches of a warp in large calls (2: 103 us, 8: 92 us)
 
 __device__ __forceinline__ uint4 ld8(const uint16_t* p) { return __ldg(reinterpret_cast<const uint4*>(p)); }
 
@@ -152,6 +156,33 @@ __device__ __forceinline__ Runs query_runs(int j, int rot) {
   return {16 * j, 16 * j + 8, false};
 }
 
+// Run k of a row (channels from 8 k): the lane that holds it in the half
+// layout's order, as its first or second.
+struct Holder {
+  int lane;
+  bool second;
+};
+__device__ __forceinline__ Holder holder_of(int k, int rot, int row_lane0) {
+  const int hr = rot / 16;
+  return {row_lane0 + (k < hr ? k : k < 2 * hr ? k - hr : k / 2), k < hr ? false : k < 2 * hr ? true : (k & 1) != 0};
+}
+
+// row_rstd when a lane's runs are any two of the row; h: who holds runs 2 j and 2 j + 1.
+template <int D>
+__device__ __forceinline__ float row_rstd_runs(const Eight& v0, const Eight& v1, const Holder (&h)[2], float eps, unsigned mask) {
+  const float s0 = squares8(v0), s1 = squares8(v1);
+  float p[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const float x = __shfl_sync(mask, s0, h[i].lane), y = __shfl_sync(mask, s1, h[i].lane);
+    p[i] = h[i].second ? y : x;
+  }
+  float t = p[0] + p[1];
+#pragma unroll
+  for (int off = 1; off < D / 16; off <<= 1) t = t + __shfl_xor_sync(mask, t, off);
+  return rstd_of(t, 1.0f / D, eps);
+}
+
 template <int D, int BITS>
 __device__ __forceinline__ void quantize_row16(const uint32_t (&w)[8], uint8_t* codes, float* sz, int j, int lpg,
                                                unsigned mask, float one, bool reciprocal) {
@@ -190,8 +221,7 @@ __device__ __forceinline__ long long slot_row(const RopeAppendArgs& a, long long
   return (page * a.Hkv + g) * a.page_tokens + slot % a.page_tokens;
 }
 
-// Query heads [h0, h1) of token t.  WHOLE: half layout with every channel
-// turning, where the sum of squares needs no other channels than the lane's.
+// Query heads [h0, h1) of token t.  WHOLE: half layout with every channel turning.
 template <int D, bool INTER, bool WHOLE>
 __device__ __forceinline__ void query_rows(const RopeAppendArgs& a, int t, int pos, int h0, int h1) {
   constexpr int LPR = D / kDimsPerLane, RPW = 32 / LPR;
@@ -199,16 +229,15 @@ __device__ __forceinline__ void query_rows(const RopeAppendArgs& a, int t, int p
   const unsigned mask = row_lane_mask<LPR>(lane);
   const Runs run = WHOLE ? Runs{8 * j, D / 2 + 8 * j, true} : query_runs<INTER>(j, a.rot);
   const bool norm = a.q_weight != nullptr;
-  const bool square = norm && !INTER && !WHOLE;  // the sum wants adjacent channels, the pairs others
+  const Holder hold[2] = {holder_of(2 * j, a.rot, lane - j), holder_of(2 * j + 1, a.rot, lane - j)};
   const uint16_t* src = a.q + t * a.q_stride;
   uint16_t* dst = a.q_out + (long long)t * a.Hq * D;
-  uint4 ua = make_uint4(0, 0, 0, 0), ub = ua, s0 = ua, s1 = ua;
+  uint4 ua = make_uint4(0, 0, 0, 0), ub = ua;
   auto fetch = [&](int h) {
     if (h >= h1) return;
     const uint16_t* row = src + (long long)h * D;
     ua = ld8(row + run.a);
     ub = ld8(row + run.b);
-    if (square) { s0 = ld8(row + 16 * j); s1 = ld8(row + 16 * j + 8); }
   };
   fetch(h0 + sub);
   Eight wa, wb;
@@ -226,12 +255,11 @@ __device__ __forceinline__ void query_rows(const RopeAppendArgs& a, int t, int p
   }
   for (int h = h0 + sub; h - sub < h1; h += RPW) {
     Eight x = widen8(ua), y = widen8(ub);
-    const uint4 q0 = s0, q1 = s1;
     fetch(h + RPW);
     if (h >= h1) continue;  // the lanes of a row agree
     if (norm) {
       const float r = WHOLE ? row_rstd_halves<D>(x, y, a.eps, mask)
-                            : square ? row_rstd<D>(widen8(q0), widen8(q1), a.eps, mask) : row_rstd<D>(x, y, a.eps, mask);
+                      : INTER ? row_rstd<D>(x, y, a.eps, mask) : row_rstd_runs<D>(x, y, hold, a.eps, mask);
       norm8(x, r, wa);
       norm8(y, r, wb);
     }
@@ -250,61 +278,56 @@ __device__ __forceinline__ void query_rows(const RopeAppendArgs& a, int t, int p
 
 // Key and value heads g0 .. of token t, one batch of 32 / (D / 16) rows.
 // All loads of the rows come before the first use, the slot's among them.
-template <int D, bool INTER>
+// In the half layout keys turn in the lanes' query runs and go through shared
+// memory into the quantizer's order.
+template <int D, bool INTER, bool WHOLE>
 __device__ __forceinline__ void key_value_rows(const RopeAppendArgs& a, int t, int pos, int g0, bool keys, bool values) {
   constexpr int LPR = D / kDimsPerLane;
   const int lane = threadIdx.x & 31, j = lane % LPR, g = g0 + lane / LPR;
   const unsigned mask = row_lane_mask<LPR>(lane);
   if (g >= a.Hkv) return;
+  const Runs run = WHOLE ? Runs{8 * j, D / 2 + 8 * j, true} : query_runs<INTER>(j, a.rot);
+  const bool norm = a.k_weight != nullptr;
   const uint16_t* src = a.k + t * a.k_stride + (long long)g * D;
   const uint16_t* vsrc = a.v + t * a.v_stride + (long long)g * D + 16 * j;
-  const int half = a.rot / 2;
-  const uint4 k0 = ld8(src + 16 * j), k1 = ld8(src + 16 * j + 8);
-  uint4 other[2] = {k0, k1};  // the partners of the lane's runs of 8 channels (half layout)
-  if constexpr (!INTER) {
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int c0 = 16 * j + 8 * e;
-      if (c0 < a.rot) other[e] = ld8(src + (c0 < half ? c0 + half : c0 - half));
-    }
-  }
+  const uint4 k0 = ld8(src + run.a), k1 = ld8(src + run.b);
   uint4 v0 = k0, v1 = k1;
   if (values) { v0 = ld8(vsrc); v1 = ld8(vsrc + 8); }
   const long long row = slot_row(a, __ldg(reinterpret_cast<const long long*>(a.slots) + t), g);
-  if (values && row >= 0) {
+  if (row < 0) return;  // the lanes of a row agree
+  if (values) {
     const uint32_t w[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
     store_row<D>(a, a.vb, w, a.v_codes, a.v_sz, row, j, mask);
   }
   if (!keys) return;
-  Eight x[2] = {widen8(k0), widen8(k1)};
-  float r = 1.0f;
-  if (a.k_weight != nullptr) {
-    r = row_rstd<D>(x[0], x[1], a.eps, mask);
-    norm8(x[0], r, widen8(ld8(a.k_weight + 16 * j)));
-    norm8(x[1], r, widen8(ld8(a.k_weight + 16 * j + 8)));
+  Eight x = widen8(k0), y = widen8(k1);
+  if (norm) {
+    const Holder hold[2] = {holder_of(2 * j, a.rot, lane - j), holder_of(2 * j + 1, a.rot, lane - j)};
+    const float r = WHOLE ? row_rstd_halves<D>(x, y, a.eps, mask)
+                    : INTER ? row_rstd<D>(x, y, a.eps, mask) : row_rstd_runs<D>(x, y, hold, a.eps, mask);
+    norm8(x, r, widen8(ld8(a.k_weight + run.a)));
+    norm8(y, r, widen8(ld8(a.k_weight + run.b)));
   }
-#pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    const int c0 = 16 * j + 8 * e;
-    if (c0 >= a.rot) continue;
+  if (run.turn) {  // 8 pairs from 8 j
+    const float* at = a.table + ((long long)pos * (WHOLE ? D / 2 : a.rot / 2) + 8 * j) * 2;
     if constexpr (INTER) {
-      const float4* p = reinterpret_cast<const float4*>(a.table + (long long)pos * a.rot + c0);
-      turn_adjacent(x[e], __ldg(p), __ldg(p + 1), a.one);
+      const float4* p = reinterpret_cast<const float4*>(at);
+      turn_adjacent(x, __ldg(p), __ldg(p + 1), a.one);
+      turn_adjacent(y, __ldg(p + 2), __ldg(p + 3), a.one);
     } else {
-      const bool low = c0 < half;
-      Eight o = widen8(other[e]);
-      if (a.k_weight != nullptr) norm8(o, r, widen8(ld8(a.k_weight + (low ? c0 + half : c0 - half))));
-      const Turns cs = load_turns(a.table + ((long long)pos * half + (low ? c0 : c0 - half)) * 2);
-      // the first of a pair: a c + b (-s); the second: b c + a s
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        x[e].e[i] = sum_of_products(exact_mul2(x[e].e[i], cs.c.e[i]), exact_mul2(o.e[i], low ? neg2(cs.s.e[i]) : cs.s.e[i]), a.one);
-        x[e].o[i] = sum_of_products(exact_mul2(x[e].o[i], cs.c.o[i]), exact_mul2(o.o[i], low ? neg2(cs.s.o[i]) : cs.s.o[i]), a.one);
-      }
+      turn_halves(x, y, load_turns(at), a.one);
     }
   }
-  if (row < 0) return;  // the lanes of a row agree
-  const uint4 n0 = narrow8(x[0]), n1 = narrow8(x[1]);
+  uint4 n0 = narrow8(x), n1 = narrow8(y);
+  if constexpr (!INTER) {
+    __shared__ uint4 s_run[kWarps][64];  // the rows' runs of 8 channels in order
+    uint4* of_row = s_run[threadIdx.x / 32] + lane / LPR * 2 * LPR;
+    of_row[run.a / 8] = n0;
+    of_row[run.b / 8] = n1;
+    __syncwarp(mask);
+    n0 = of_row[2 * j];
+    n1 = of_row[2 * j + 1];
+  }
   const uint32_t w[8] = {n0.x, n0.y, n0.z, n0.w, n1.x, n1.y, n1.z, n1.w};
   store_row<D>(a, a.kb, w, a.k_codes, a.k_sz, row, j, mask);
 }
@@ -317,7 +340,7 @@ __device__ __forceinline__ void prefetch_lines(const void* p, int bytes, int lan
 // One warp: one token and one of its items -- query runs, then key and value
 // batches.
 template <int D, bool INTER, bool WHOLE>
-__global__ void __launch_bounds__(32 * kWarps, kBlocksPerSm) rope_append_kernel(RopeAppendArgs a, int q_items, int kv_items) {
+__global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(WHOLE)) rope_append_kernel(RopeAppendArgs a, int q_items, int kv_items) {
   constexpr int RPW = 32 / (D / kDimsPerLane);
   const int items = q_items + kv_items;
   const long long id = (long long)blockIdx.x * kWarps + threadIdx.x / 32;
@@ -346,7 +369,7 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocksPerSm) rope_append_kernel(
     query_rows<D, INTER, WHOLE>(a, (int)t, pos, h0, h1);
   } else {
     const bool second = a.split && ((item - q_items) & 1);
-    key_value_rows<D, INTER>(a, (int)t, pos, g0, !second, !a.split || second);
+    key_value_rows<D, INTER, WHOLE>(a, (int)t, pos, g0, !second, !a.split || second);
   }
 }
 
@@ -360,7 +383,7 @@ cudaError_t launch_t(RopeAppendArgs a, cudaStream_t s) {
   a.split = !many;
   const int q_items = (a.Hq + RPW * a.iters - 1) / (RPW * a.iters), kv_items = (a.Hkv + RPW - 1) / RPW * (many ? 1 : 2);
   // tokens that the resident warps hold at a time
-  a.ahead = many ? (int)((long long)num_sms() * kBlocksPerSm * kWarps / (q_items + kv_items)) + 1 : 0;
+  a.ahead = many ? (int)((long long)num_sms() * blocks_per_sm(WHOLE) * kWarps / (q_items + kv_items)) + 1 : 0;
   const long long blocks = ((long long)a.n_cap * (q_items + kv_items) + kWarps - 1) / kWarps;
   if (blocks >= (1ll << 31)) return cudaErrorInvalidValue;
   rope_append_kernel<D, INTER, WHOLE><<<(unsigned)blocks, 32 * kWarps, 0, s>>>(a, q_items, kv_items);

@@ -180,3 +180,10 @@ def test_two_calls_on_two_streams(orc):
     torch.cuda.synchronize()
     for x, y in zip(c, one):
         assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("D,rot", [(64, 0), (64, 16), (64, 48), (128, 0), (128, 16), (128, 48), (128, 80), (128, 112)])
+@pytest.mark.parametrize("N", [3, 1500])
+def test_norm_with_some_channels_turning(orc, D, rot, N):
+    """The norm's sum runs over adjacent channels while the lanes hold pairs; large calls take runs of heads."""
+    run(orc, N=N, Hq=33, Hkv=5, D=D, G=32, rot=rot, norm=True, seed=N + rot)
