@@ -446,3 +446,16 @@ def test_serving_step(orc):
         want, _ = ref.attention(qr, kh, vh, L, np.cumsum([0] + list(news)), float(np.float32(D ** -0.5)), softcap=30.0, window=300)
         close(out[:n].cpu().numpy(), want, float(np.abs(vh).max()))
         assert lens.tolist() == L
+
+
+@pytest.mark.parametrize("n", [1, 4])
+@pytest.mark.parametrize("kw", [dict(), dict(slopes=True), dict(prefix=(50000,), starts=(59990,)), dict(softcap=5.0, window=40000)])
+def test_one_unit_across_the_grid(orc, n, kw):
+    """Every CTA holds a piece of the only unit; with a distance bias the references of the pieces rise by thousands."""
+    case(orc, lens=(60000,), Hkv=1, n=n, seed=61, **kw)
+
+
+@pytest.mark.parametrize("kb,vb,D,G", [(8, 8, 128, 32), (16, 16, 128, 64), (4, 2, 64, 32)])
+def test_few_units_across_the_grid(orc, kb, vb, D, G):
+    """Units of several CTAs whose ends lie inside CTAs: one CTA arrives at two units."""
+    case(orc, kb, vb, G, D=D, lens=(9001, 8123, 33), Hkv=1, r=8, n=3, seed=62, slopes=True)
