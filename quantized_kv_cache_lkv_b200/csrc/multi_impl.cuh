@@ -22,16 +22,19 @@
 //     N = 8 columns: with 1 to 8 query rows nothing but columns is padded;
 //   - K codes become fp16 integers against q scaled by a power of two
 //     (mma_k.cuh): exact products.  V codes become fp16 integers against
-//     e * scale split in two fp16 terms (22 bits), the scales taken relative
-//     to a power of two above them so that e * scale stays below 2^15.  At the
-//     16-bit width both products are bf16, e split in three terms;
+//     e * scale split in two fp16 terms (22 bits), in a unit of its own for each
+//     query row and channel group: a power of two that keeps e * scale below
+//     2^15 and moves only when one passes that.  It follows the products and not
+//     the scales, since a token of large scale may have no weight, and a small
+//     group may stand beside a large one.  At the 16-bit width both products are
+//     bf16, e split in three terms;
 //   - the channel-to-row and token-to-slot orders of the MMAs are free, so
 //     every lane reads whole runs of codes of one token from shared memory,
 //     and the codes of two tokens are paired by one byte permute per half
 //     word, before they are unpacked;
-//   - what depends on a token alone -- centring, the check of the scales, the
-//     zeroing of what nobody sees -- is done once, by the lane of that token,
-//     in the tile's (scale, zero) rows in shared memory;
+//   - what depends on a token alone -- centring, the zeroing of what nobody
+//     sees -- is done once, by the lane of that token, in the tile's (scale, zero)
+//     rows in shared memory;
 //   - the reference exponent is an integer and moves only when a score passes
 //     it by 2^8, so rescaling is rare and exact.
 //
@@ -45,9 +48,9 @@
 // in order, so results do not depend on timing.
 //
 // Measured on a B200, device time: K6V4, B16 x 8192, 32 / 8 heads, capped and
-// paged: 74 us for 201.7 MB (2.7 TB/s); 16 query rows over 131072 tokens: 114 us;
-// 8-bit, G 32, 64 ragged sequences behind a window of 1024: 58 us for 167 MB.
-// 1030 instructions a tile of 32 tokens, half of the issue slots used.
+// paged: 73 us for 201.7 MB (2.7 TB/s); 16 query rows over 131072 tokens: 123 us
+// (113 before the units followed the products: 7% more instructions); 8-bit, G 32,
+// 64 ragged sequences behind a window of 1024: 59 us for 167 MB.
 #pragma once
 #include <type_traits>
 
@@ -65,7 +68,18 @@ constexpr unsigned kFull = 0xFFFFFFFFu;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLazy = 8.0f;      // the reference moves when a score passes it by 2^8
-constexpr int kTop = 7;            // scales are brought to at most 2^(kTop - 1): e * scale stays below 2^14
+// Units of e * scale in fp16: a row whose products may reach 2^15 (fp16 ends at
+// 65504) has them moved.  The bound is the row's largest e times the tile's
+// largest scale.  Where the tile's scales lie within 2^kNarrow, the largest
+// product is at least 2^-(kNarrow + 2) of it, good enough to place a unit by: one
+// power moves all groups of the row and the bound comes to 2^kPlace, that of the
+// smallest group to 2^(kPlace - kSpread) or more.  Elsewhere the largest product of
+// each group is found and comes to 2^kPlace itself.  What fp16 drops, 2^-25, is
+// then 2^-25 of a group's largest product at worst and 2^-33 as a rule.
+constexpr int kOverExp = 15, kPlace = 8;
+constexpr unsigned kNarrow = 3, kSpread = 3, kLeast = 127 - 90;  // the last: from 2^-90 the units are normal numbers
+constexpr float kOver = (float)(1 << kOverExp);
+constexpr int kUnitMax = 126;  // its inverse is a normal number
 
 __device__ __forceinline__ float ex2(float x) {  // 2^x; -inf gives 0
   float y;
@@ -107,6 +121,9 @@ __device__ __forceinline__ void hmma16816_bf16_first(float (&c)[4], uint32_t a0,
       : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
+
+// The exponent of a positive normal number.
+__device__ __forceinline__ int exponent_of(float x) { return (int)(__float_as_uint(x) >> 23) - 127; }
 
 // 2^n for an integer-valued n; 0 below the normal range.
 __device__ __forceinline__ float pow2i(float n) {
@@ -291,7 +308,7 @@ struct Work {
   float ref[C::NT], l[C::NT]; // reference exponent (an integer) and sum of e (this lane's tokens), row gid
   bool live[C::NT];           // the row has seen a token
   float refc[C::NT][2];       // references of columns 2 tig and 2 tig + 1 (0 when scores are capped)
-  float top;                  // o is in units of top * 2^-kTop, a power of two above the V scales seen
+  float u[C::NT][C::NG];      // o of row gid is the output times 2^-ref times this, a power of two (quantized V)
   int orow[C::NT];            // row gid's place in out: row * Hq + head
   uint32_t qf[C::NT][C::BLK][8];
   float ka[C::NT][2];              // factor of the code product, columns 2 tig and 2 tig + 1
@@ -316,7 +333,6 @@ __device__ __forceinline__ void load_unit(const MultiArgs& a, const Seq& s, int 
   w.p_max = s.T - s.n + i1;
   w.lo_min = max(s.start, a.window > 0 ? w.p_min - a.window + 1 : 0);
   w.lo_max = max(s.start, a.window > 0 ? w.p_max - a.window + 1 : 0);
-  w.top = pow2i(-126.0f + kTop);
 #pragma unroll
   for (int mt = 0; mt < C::MT; ++mt)
 #pragma unroll
@@ -348,7 +364,10 @@ __device__ __forceinline__ void load_unit(const MultiArgs& a, const Seq& s, int 
     // sums of q over each group, and its largest magnitude
     float big = 0.0f, sum[C::NG];
 #pragma unroll
-    for (int gi = 0; gi < C::NG; ++gi) sum[gi] = w.zacc[nt][gi] = 0.0f;
+    for (int gi = 0; gi < C::NG; ++gi) {
+      sum[gi] = w.zacc[nt][gi] = 0.0f;
+      w.u[nt][gi] = pow2i((float)kUnitMax);
+    }
 #pragma unroll
     for (int blk = 0; blk < C::BLK; ++blk) {
       float t = 0.0f;
@@ -428,10 +447,11 @@ constexpr uint32_t kRoundBits = 0x4B400000u;
 
 // The lane of a token readies its (scale, zero) rows: K's zero becomes the
 // value of the code nearest 0 (the code itself goes to cen), V's that of the
-// middle code, and V's scale is taken relative to w.top, which is raised (and
-// the output rescaled) when a scale passes it.  What no row sees becomes 0 in V.
+// middle code.  What no row sees becomes 0 in V.  big: the largest V scale of
+// each group, as bits.
 template <typename C>
-__device__ __forceinline__ void ready_tokens(Work<C>& w, uint8_t* stage, uint32_t* cen, int t0, bool whole) {
+__device__ __forceinline__ void ready_tokens(const Work<C>& w, uint8_t* stage, uint32_t* cen, int t0, bool whole,
+                                             unsigned (&big)[C::NG]) {
   const int lane = threadIdx.x & 31;
   const bool mine = C::TT == 32 || lane < C::TT;
   const int t = t0 + lane;
@@ -459,33 +479,21 @@ __device__ __forceinline__ void ready_tokens(Work<C>& w, uint8_t* stage, uint32_
     }
   }
   if constexpr (C::VB < 16) {
-    float* vsz = reinterpret_cast<float*>(stage + C::OFF_VSZ) + lane * C::NG * 2;
+    float2* vsz = reinterpret_cast<float2*>(stage + C::OFF_VSZ) + lane * C::NG;
     float2 v[C::NG];
-    float big = 0.0f;
 #pragma unroll
     for (int gi = 0; gi < C::NG; ++gi) {
       v[gi] = make_float2(0.0f, 0.0f);
-      if (mine && alive) v[gi] = *reinterpret_cast<const float2*>(vsz + 2 * gi);
-      big = fmaxf(big, v[gi].x);
+      if (mine && alive) v[gi] = vsz[gi];
     }
-    if (__any_sync(kFull, big > w.top)) {
 #pragma unroll
-      for (int off = 16; off >= 1; off >>= 1) big = fmaxf(big, __shfl_xor_sync(kFull, big, off));
-      // a power of two at least twice as large
-      const float top = pow2i((float)((int)(__float_as_uint(big) >> 23) - 127 + 2)), f = w.top * (1.0f / top);
-      w.top = top;
-#pragma unroll
-      for (int mt = 0; mt < C::MT; ++mt)
-#pragma unroll
-        for (int nt = 0; nt < C::NT; ++nt)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) w.o[mt][nt][i] *= f;
+    for (int gi = 0; gi < C::NG; ++gi) {
+      big[gi] = __reduce_max_sync(kFull, __float_as_uint(fabsf(v[gi].x)));
+      v[gi].y = fmaf((float)(1 << (C::VB - 1)), v[gi].x, v[gi].y);
     }
-    const float rel = (float)(1 << kTop) / w.top;
     if (mine) {
 #pragma unroll
-      for (int gi = 0; gi < C::NG; ++gi)
-        *reinterpret_cast<float2*>(vsz + 2 * gi) = make_float2(v[gi].x * rel, fmaf((float)(1 << (C::VB - 1)), v[gi].x, v[gi].y));
+      for (int gi = 0; gi < C::NG; ++gi) vsz[gi] = v[gi];
     }
   } else if (!whole) {
     unsigned gone = __ballot_sync(kFull, mine && !alive);
@@ -617,6 +625,39 @@ __device__ __forceinline__ void k_product(const uint8_t* kc, const uint32_t* cen
 }
 
 // ------------------------------------------------------------------ output
+// Sets each row's and group's unit by its largest product in the tile; x: the
+// exponents of e.  A unit rises by at most 2^by[nt], what the row's reference has
+// risen by.
+template <typename C>
+__device__ __forceinline__ void set_units(Work<C>& w, const float* vsz, const float (&x)[C::TS][C::NT][4], const float (&by)[C::NT]) {
+  constexpr int PER = C::MT / C::NG;  // m-tiles of a group
+  const int tig = threadIdx.x & 3;
+#pragma unroll
+  for (int gi = 0; gi < C::NG; ++gi)
+#pragma unroll
+    for (int nt = 0; nt < C::NT; ++nt) {
+      float t = 0.0f;
+#pragma unroll
+      for (int ts = 0; ts < C::TS; ++ts)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) t = fmaxf(t, fabsf(ex2(x[ts][nt][j]) * vsz[((16 * ts + tig + 4 * j) * C::NG + gi) * 2]));
+      t = fmaxf(t, __shfl_xor_sync(kFull, t, 1));
+      t = fmaxf(t, __shfl_xor_sync(kFull, t, 2));
+      const float at = (float)exponent_of(w.u[nt][gi]);
+      float to = fminf(at + by[nt], (float)kUnitMax);
+      if (t * pow2i(to) >= kOver) to = (float)(kPlace - exponent_of(t));
+      w.u[nt][gi] = pow2i(to);
+      const float f = pow2i(to - at - by[nt]);
+      const float f0 = __shfl_sync(kFull, f, 8 * tig), f1 = __shfl_sync(kFull, f, 8 * tig + 4);
+#pragma unroll
+      for (int mt = 0; mt < PER; ++mt) {
+        float(&o)[4] = w.o[gi * PER + mt][nt];
+        o[0] *= f0; o[1] *= f1;
+        o[2] *= f0; o[3] *= f1;
+      }
+    }
+}
+
 // o += sum over 16 tokens of (e * scale) code: rows = channels, slots 2 tig,
 // 2 tig + 1, 2 tig + 8, 2 tig + 9 = tokens tig, tig + 4, tig + 8, tig + 12.
 template <typename C>
@@ -640,9 +681,9 @@ __device__ __forceinline__ void v_product(const uint8_t* vc, const float* vsz, W
 #pragma unroll
         for (int j = 0; j < 4; ++j) sz[j][gi] = *reinterpret_cast<const float2*>(szb + (4 * j * C::NG + gi) * 2);
       }
+      if constexpr (VB == 16) {
 #pragma unroll
-      for (int nt = 0; nt < C::NT; ++nt) {
-        if constexpr (VB == 16) {
+        for (int nt = 0; nt < C::NT; ++nt)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             const float x = e[nt][2 * j], y = e[nt][2 * j + 1];
@@ -653,17 +694,19 @@ __device__ __forceinline__ void v_product(const uint8_t* vc, const float* vsz, W
             pw[nt][1][j] = m;
             pw[nt][2][j] = pack_bf16(xr - bf16_lo(m), yr - bf16_hi(m));
           }
-        } else {
+      } else {
+#pragma unroll
+        for (int nt = 0; nt < C::NT; ++nt)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            const float x = e[nt][2 * j] * sz[2 * j][gi].x, y = e[nt][2 * j + 1] * sz[2 * j + 1][gi].x;
+            const float2 eu = exact_mul2(make_float2(e[nt][2 * j], e[nt][2 * j + 1]), f2(w.u[nt][gi]));
+            const float x = eu.x * sz[2 * j][gi].x, y = eu.y * sz[2 * j + 1][gi].x;
             w.zacc[nt][gi] = fmaf(e[nt][2 * j], sz[2 * j][gi].y, fmaf(e[nt][2 * j + 1], sz[2 * j + 1][gi].y, w.zacc[nt][gi]));
             const uint32_t h = pack_f16(x, y);
             const float2 f = unpack_f16(h);
             pw[nt][0][j] = h;
             pw[nt][1][j] = pack_f16(x - f.x, y - f.y);
           }
-        }
       }
     }
     uint32_t r[4][N];
@@ -691,14 +734,15 @@ __device__ __forceinline__ void v_product(const uint8_t* vc, const float* vsz, W
 // One staged tile from position t0: scores, running softmax, output.
 template <typename C>
 __device__ __forceinline__ void tile_step(const MultiArgs& a, Work<C>& w, uint8_t* stage, float* tr, int t0) {
-  constexpr int TS = C::TS, NT = C::NT, NG = C::NG;
+  constexpr int TS = C::TS, TT = C::TT, NT = C::NT, NG = C::NG;
   const int lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
   uint32_t* cen = reinterpret_cast<uint32_t*>(tr + Scratch<C>::kScores);
   const float* ksz = reinterpret_cast<const float*>(stage + C::OFF_KSZ);
   const float* vsz = reinterpret_cast<const float*>(stage + C::OFF_VSZ);
   const int t1 = t0 + C::TT - 1;
   const bool whole = (t0 >= w.lo_max && t1 <= w.p_min) || t1 < w.pre;  // p_min and pre lie before T
-  ready_tokens<C>(w, stage, cen, t0, whole);
+  unsigned big[NG];
+  ready_tokens<C>(w, stage, cen, t0, whole, big);
 #pragma unroll
   for (int ts = 0; ts < TS; ++ts) {
     float acc[C::AC][NT][4];
@@ -804,15 +848,55 @@ __device__ __forceinline__ void tile_step(const MultiArgs& a, Work<C>& w, uint8_
     t = fmaxf(t, __shfl_xor_sync(kFull, t, 2));
     mx[nt] = t;
     grow |= t > (w.live[nt] ? kLazy : -INFINITY);
+    if constexpr (C::VB < 16) {
+      // a bound of the row's products: exponents of its largest e, of the tile's largest scale and of the unit.  A moving
+      // reference does not change it (e falls as the unit rises)
+      unsigned k = 0;
+#pragma unroll
+      for (int gi = 0; gi < NG; ++gi) k = max(k, big[gi] + __float_as_uint(w.u[nt][gi]));
+      grow |= __float2int_ru(t) > kOverExp + 2 * 127 - 1 - (int)(k >> 23);
+    }
   }
-  if (__any_sync(kFull, grow)) {
+  const bool slow = __any_sync(kFull, grow);
+  if (slow) {
+    // one power for all groups of a row will do while the tile's scales lie close together
+    bool easy = true;
+    if constexpr (C::VB < 16) {
+      const int t = t0 + lane;
+      if ((TT == 32 || lane < TT) && (whole || (t < w.T && (t < w.pre || (t >= w.lo_min && t <= w.p_max))))) {
+#pragma unroll
+        for (int gi = 0; gi < NG; ++gi) easy &= __float_as_uint(fabsf(vsz[(lane * NG + gi) * 2])) + (kNarrow << 23) >= big[gi];
+      }
+#pragma unroll
+      for (int gi = 0; gi < NG; ++gi) easy &= big[gi] >= kLeast << 23;
+    }
+    float f[NT], d[NT], up[NT];  // factor of o, and what the units rise by: all as one, or at most
+    bool exact = false;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       const bool any = mx[nt] > -INFINITY;
       const float most = any ? ceilf(mx[nt] + w.ref[nt]) : w.ref[nt];
       const float ref = w.live[nt] ? fmaxf(w.ref[nt], most) : most;
-      w.live[nt] |= any;
       const float by = ref - w.ref[nt], al = pow2i(-by);
+      f[nt] = al;
+      if constexpr (C::VB < 16) {
+        // o keeps its value where the units take the factor up: what is small beside the old reference may matter now
+        // (past 2^400 nothing is left of it, and larger powers would round)
+        up[nt] = d[nt] = w.live[nt] ? fminf(by, 400.0f) : 0.0f;
+        unsigned k0 = 0xFFFFFFFFu, k1 = 0;
+#pragma unroll
+        for (int gi = 0; gi < NG; ++gi) {
+          k0 = min(k0, big[gi] + __float_as_uint(w.u[nt][gi]));
+          k1 = max(k1, big[gi] + __float_as_uint(w.u[nt][gi]));
+        }
+        const float over = ceilf(mx[nt] - by) + d[nt] + (float)((int)(k1 >> 23) - (2 * 127 - 1) - kPlace);  // of the bound
+        if (over > 0.0f) {
+          d[nt] -= over;
+          easy &= k1 - k0 <= kSpread << 23;
+        }
+        f[nt] = pow2i(d[nt] - by);
+      }
+      w.live[nt] |= any;
       w.ref[nt] = ref;
       w.l[nt] *= al;
 #pragma unroll
@@ -821,14 +905,26 @@ __device__ __forceinline__ void tile_step(const MultiArgs& a, Work<C>& w, uint8_
       for (int ts = 0; ts < TS; ++ts)
 #pragma unroll
         for (int j = 0; j < 4; ++j) e[ts][nt][j] -= by;
-      const float a0 = __shfl_sync(kFull, al, 8 * tig), a1 = __shfl_sync(kFull, al, 8 * tig + 4);
       const float r0 = __shfl_sync(kFull, ref, 8 * tig), r1 = __shfl_sync(kFull, ref, 8 * tig + 4);
       if (a.softcap <= 0.0f) { w.refc[nt][0] = r0; w.refc[nt][1] = r1; }
+    }
+    if constexpr (C::VB < 16) exact = !__all_sync(kFull, easy);
+    if (!exact) {
 #pragma unroll
-      for (int mt = 0; mt < C::MT; ++mt) {
-        w.o[mt][nt][0] *= a0; w.o[mt][nt][1] *= a1;
-        w.o[mt][nt][2] *= a0; w.o[mt][nt][3] *= a1;
+      for (int nt = 0; nt < NT; ++nt) {
+        if constexpr (C::VB < 16) {
+#pragma unroll
+          for (int gi = 0; gi < NG; ++gi) w.u[nt][gi] = __uint_as_float(__float_as_uint(w.u[nt][gi]) + ((unsigned)(int)d[nt] << 23));
+        }
+        const float a0 = __shfl_sync(kFull, f[nt], 8 * tig), a1 = __shfl_sync(kFull, f[nt], 8 * tig + 4);
+#pragma unroll
+        for (int mt = 0; mt < C::MT; ++mt) {
+          w.o[mt][nt][0] *= a0; w.o[mt][nt][1] *= a1;
+          w.o[mt][nt][2] *= a0; w.o[mt][nt][3] *= a1;
+        }
       }
+    } else {
+      if constexpr (C::VB < 16) set_units<C>(w, vsz, e, up);
     }
   }
 #pragma unroll
@@ -861,7 +957,6 @@ __device__ __forceinline__ void flush(const MultiArgs& a, Work<C>& w, float* pie
   constexpr int NT = C::NT, NG = C::NG;
   const int lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
   const int rows = min(8 * NT, w.n * a.r - w.rb * 8 * NT);
-  const float unit = w.top * (1.0f / (float)(1 << kTop));
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     float l = w.l[nt];
@@ -888,9 +983,12 @@ __device__ __forceinline__ void flush(const MultiArgs& a, Work<C>& w, float* pie
       const int src = 4 * (2 * tig + j), col = nt * 8 + 2 * tig + j;
       const float lc = __shfl_sync(kFull, l, src);
       const int orow = __shfl_sync(kFull, w.orow[nt], src);
-      float z[NG];
+      float z[NG], unit[NG];
 #pragma unroll
-      for (int gi = 0; gi < NG; ++gi) z[gi] = __shfl_sync(kFull, w.zacc[nt][gi], src);
+      for (int gi = 0; gi < NG; ++gi) {
+        z[gi] = __shfl_sync(kFull, w.zacc[nt][gi], src);
+        unit[gi] = pow2i((float)-exponent_of(__shfl_sync(kFull, w.u[nt][gi], src)));
+      }
       const float f = piece != nullptr ? 1.0f : (lc > 0.0f ? 1.0f / lc : 0.0f);
       if (col < rows) {
         float* dst = piece != nullptr ? piece + 16 * NT + col * C::D : a.out + (long long)orow * C::D;
@@ -900,8 +998,9 @@ __device__ __forceinline__ void flush(const MultiArgs& a, Work<C>& w, float* pie
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const int c = ((mt + i / 2) % C::TPB) * 2 + (i & 1);  // the code's place in its run
-            const float x = w.o[mt + i / 2][nt][2 * (i & 1) + j] * (C::VB == 16 ? 1.0f : unit * (1.0f / (float)(1 << code_off<C::VB>(c))));
-            y[i] = (C::VB == 16 ? x : x + z[mt / C::TPB / C::GRUNS]) * f;
+            const int gi = mt / C::TPB / C::GRUNS;
+            const float x = w.o[mt + i / 2][nt][2 * (i & 1) + j];
+            y[i] = (C::VB == 16 ? x : fmaf(x * (1.0f / (float)(1 << code_off<C::VB>(c))), unit[gi], z[gi])) * f;
           }
           *reinterpret_cast<float4*>(dst + out_channel<C>(mt, 0, gid)) = make_float4(y[0], y[1], y[2], y[3]);
         }
