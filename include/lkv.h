@@ -512,7 +512,7 @@ LKV_API int lkv_rope_append_kv(lkv_qspec spec, int n_cap, int Hq, int Hkv, int n
 /* Scores and visibility of lkv_decode_attention_multi. */
 typedef struct {
     float softmax_scale;        /* finite, and so are softmax_scale / c and softmax_scale * log2(e) */
-    float softcap;              /* c >= 1e-30: scores become c * tanh(score / c); 0: none */
+    float softcap;              /* c >= 1e-30: scores become c * tanh(score / c); 0: none, and above 1e30 none either */
     int32_t window;             /* w > 0: a query sees the last w positions, its own among them; 0: all */
     const float *slopes;        /* device f32 [Hq], nullable: slopes[h] * (t - p) is added to the score */
     const int32_t *prefix_lens; /* device int32 [B], nullable: positions before it are visible to every query */

@@ -47,6 +47,9 @@ int multi_impl(lkv_qspec spec, int B, int Hq, int Hkv, int T_cap, int D, int max
     return LKV_ERR_INVALID_ARG;
   // scores are divided by the cap: a smaller one takes them out of fp32
   if (rule.softcap > 0.0f && rule.softcap < 1e-30f) return LKV_ERR_INVALID_ARG;
+  // c tanh(x / c) = x (1 - (x / c)^2 / 3 + ...) is x to fp32 for |x| < c 2^-12: above 1e30 a cap only takes x / c out of
+  // the normal numbers and c log2(e) to infinity
+  if (rule.softcap > 1e30f) rule.softcap = 0.0f;
   // the factor of q . khat; an infinite one would make NaN of a product that is 0
   if (!std::isfinite(rule.softcap > 0.0f ? rule.softmax_scale / rule.softcap : rule.softmax_scale * 1.442695f))
     return LKV_ERR_INVALID_ARG;

@@ -214,3 +214,9 @@ def test_reciprocal_is_a_flag(flag, want):
                                             (1e-38, 1e-30, 0)])
 def test_score_factor_is_finite(scale, cap, want):
     assert rc_of(lkv.lkv_decode_attention_multi, **multi_args(rule=rule(softmax_scale=scale, softcap=cap), n_rows=0, q=None, out=None)) == want
+
+
+@pytest.mark.parametrize("scale,cap,want", [(0.1, 3.4e38, 0), (1e38, 1e31, 0), (2e38, 3e38, 0), (3e38, 3e38, ARG), (3e38, 1e30, 0)])
+def test_caps_above_1e30_are_none(scale, cap, want):
+    """Such a cap is accepted; the factor of the scores is then the scale itself."""
+    assert rc_of(lkv.lkv_decode_attention_multi, **multi_args(rule=rule(softmax_scale=scale, softcap=cap), n_rows=0, q=None, out=None)) == want
