@@ -111,6 +111,10 @@ class Args {
     return v != 0;
   }
   bool bad_flag() const { return bad_flag_; }
+  [[noreturn]] void refuse_arg(const char* what) {
+    raise(LKV_ERR_INVALID_ARG, (std::string(name_) + ": " + what).c_str());
+    throw Failed{};
+  }
 
   // A quantizer spec: an lkv_qspec or (k_bits, v_bits, group).
   lkv_qspec spec() {
@@ -138,11 +142,12 @@ class Args {
   template <typename T = void>
   T* ptr(at::ScalarType type, int64_t numel) { return static_cast<T*>(address(next(), type, numel)); }
 
+  // No tensor has room for a negative number of values.
   void* address(PyObject* o, at::ScalarType type, int64_t numel) {
     if (o == Py_None) return nullptr;
     if (PyLong_Check(o)) return number(o);
     const at::Tensor& t = tensor(o);
-    if (t.scalar_type() == type && t.numel() >= numel && t.is_contiguous() && on_device(t)) return t.data_ptr();
+    if (numel >= 0 && t.scalar_type() == type && t.numel() >= numel && t.is_contiguous() && on_device(t)) return t.data_ptr();
     refuse(t, std::to_string(numel) + " or more contiguous " + c10::toString(type));
   }
 
@@ -397,6 +402,7 @@ Tail tail(Args& a, int64_t Hq, int64_t B, int64_t rows, int64_t D) {
   t.lse = a.ptr<float>(at::kFloat, rows * Hq);
   PyObject* ws = a.object();
   t.bytes = a.i64();
+  if (t.bytes < 0) a.refuse_arg("ws_bytes is negative");  // a size_t of it would pass for all the room there is
   t.ws = a.address(ws, at::kByte, t.bytes);
   t.stream = a.stream();
   return t;

@@ -220,3 +220,16 @@ def test_score_factor_is_finite(scale, cap, want):
 def test_caps_above_1e30_are_none(scale, cap, want):
     """Such a cap is accepted; the factor of the scores is then the scale itself."""
     assert rc_of(lkv.lkv_decode_attention_multi, **multi_args(rule=rule(softmax_scale=scale, softcap=cap), n_rows=0, q=None, out=None)) == want
+
+
+@pytest.mark.parametrize("ws", [at(9), torch.zeros(64, dtype=torch.uint8), None])
+@pytest.mark.parametrize("size", [-1, -256, -(1 << 63)])
+def test_negative_workspace_size(ws, size):
+    """Not taken for 2^64 less as much, which any workspace would seem to have room for.  Nothing is launched here (no rows)."""
+    a = multi_args(workspace=ws, ws_bytes=size, n_rows=0, q=None, out=None)
+    assert rc_of(lkv.lkv_decode_attention_multi, **a) == ARG
+    a.update(pages_per_seq=4, num_pages=9, block_table=at(10))
+    for old, new in (("k_codes", "k_pool"), ("k_sz", "k_sz_pool"), ("v_codes", "v_pool"), ("v_sz", "v_sz_pool")):
+        a[new] = a.pop(old)
+    del a["T_cap"]
+    assert rc_of(lkv.lkv_decode_attention_multi_paged, **a) == ARG
