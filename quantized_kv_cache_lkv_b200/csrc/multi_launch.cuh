@@ -9,10 +9,12 @@ template <int D, int KB, int VB, int G, int NT>
 cudaError_t launch_c(const MultiArgs& a, const MultiPlan& p, cudaStream_t s) {
   using C = Cfg<D, KB, VB, G, NT>;
   static_assert(C::STAGES >= 2, "a ring of two stages");
-  const size_t smem = smem_of(p.sh, a.B);
-  const cudaError_t e = cudaFuncSetAttribute(multi_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  // the limit belongs to the kernel and not to the call: what the largest batch needs, so that calls of other batches from
+  // other threads do not lower it between this line and the launch
+  const cudaError_t e =
+      cudaFuncSetAttribute(multi_kernel<C>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_of(p.sh, kMaxBatch));
   if (e != cudaSuccess) return e;
-  multi_kernel<C><<<p.grid, 32 * C::WARPS, smem, s>>>(a);
+  multi_kernel<C><<<p.grid, 32 * C::WARPS, smem_of(p.sh, a.B), s>>>(a);
   return cudaGetLastError();
 }
 

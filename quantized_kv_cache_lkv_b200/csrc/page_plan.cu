@@ -180,7 +180,9 @@ template <int kRun>
 static cudaError_t launch_run(const PlanArgs& a, cudaStream_t s) {
   const size_t smem = (size_t)2 * (a.B + 1) * sizeof(int);
   if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(page_plan_kernel<kRun>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    // the kernel's limit, not this call's: calls of other batches from other threads set the same
+    const cudaError_t e = cudaFuncSetAttribute(page_plan_kernel<kRun>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               2 * (kPlanMaxBatch + 1) * (int)sizeof(int));
     if (e != cudaSuccess) return e;
   }
   const long long want = (std::max((long long)a.n_cap / kRun + 1, (long long)a.B) + kThreads - 1) / kThreads;
