@@ -531,7 +531,8 @@ typedef struct {
  *         lkv_score_rule)
  *   out = sum_t exp(x_t) vhat_t / sum_t exp(x_t) over the visible t
  *   lse = ln sum_t exp(x_t)
- * A query that sees nothing gets out = 0 and lse = -infinity.  Arithmetic
+ * A query that sees nothing gets out = 0 and lse = -infinity; where a score
+ * is not a number, neither are out and lse.  Arithmetic
  * keeps fp32 accuracy, and results do not depend on timing.  (scale, zero)
  * and 16-bit values at positions that no query of the sequence sees may be
  * anything, infinities and NaN among them.

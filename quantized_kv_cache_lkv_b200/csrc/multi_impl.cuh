@@ -940,7 +940,10 @@ __device__ __forceinline__ void tile_step(const MultiArgs& a, Work<C>& w, uint8_
 }
 
 // ------------------------------------------------------------------ writing a unit or a piece
-__device__ __forceinline__ float lse_of(float m, float l) { return l > 0.0f ? (m + log2f(l)) * kLn2 : -INFINITY; }
+// A sum of 0 is a row that sees nothing; one that is not a number has scores that are none, which count for no reference.
+__device__ __forceinline__ float lse_of(float m, float l) {
+  return l == 0.0f ? -INFINITY : isnan(l) ? l : (m + log2f(l)) * kLn2;
+}
 
 // A piece: (reference, sum) of 8 NT rows, then their partial outputs.
 template <int D, int NT>
