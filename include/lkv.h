@@ -474,8 +474,9 @@ LKV_API int lkv_rope_table(lkv_rope_spec spec, int rows, float *table, void *str
  * num_pages = B, page_tokens = T_cap, slot b * T_cap + t.
  *
  *   n_tokens   in  nullable int32 [1]: tokens there are (clamped into
- *                  [0, n_cap]; NULL: n_cap).  Rows behind them are not read,
- *                  and nothing is written for them
+ *                  [0, n_cap]; NULL: n_cap).  Rows of q, k and v behind them
+ *                  are not read, nothing is written for them, and what their
+ *                  positions and slots hold does not matter
  *   positions  in  int32 [n_cap] (may be NULL when rot_dim == 0); a token
  *                  whose position lies outside [0, table_rows) is left out:
  *                  nothing is written for it

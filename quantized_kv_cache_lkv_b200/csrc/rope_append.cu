@@ -19,8 +19,9 @@
 // in groups of adjacent channels: they are rotated like queries and change
 // order through shared memory (16384 tokens: 86 us, and 92 where lanes kept
 // their 16 adjacent channels and read and normed the partners too).  16384
-// tokens of 32 / 8 heads into a K6V4 cache: 85 us for 369 MB (4.3 TB/s); 16
-// tokens: 3.3 us.
+// tokens of 32 / 8 heads into a K6V4 cache: 84 us for 369 MB (4.4 TB/s); 16
+// tokens: 3.2 us, and 9.8 at a capacity of 16384 (27.5 while the rows behind the
+// count were prefetched too).
 #include <algorithm>
 
 #include "serving.cuh"
@@ -351,7 +352,10 @@ __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(WHOLE)) rope_append
   const bool query = item < q_items;
   const int h0 = item * RPW * a.iters, h1 = min(a.Hq, h0 + RPW * a.iters);
   const int kv = a.split ? (item - q_items) / 2 : item - q_items, g0 = kv * RPW, g1 = min(a.Hkv, g0 + RPW);
-  if (a.ahead > 0 && t + a.ahead < a.n_cap) {
+  const int n = a.n_tokens ? clamp_len(__ldg(a.n_tokens), a.n_cap) : a.n_cap;
+  const int pos = a.rot > 0 ? __ldg(a.positions + t) : 0;  // with the count, not behind it: one wait in a small call
+  if (t >= n) return;
+  if (a.ahead > 0 && t + a.ahead < n) {
     // the same item of a token that no resident warp has reached yet
     const long long u = t + a.ahead;
     if (query) {
@@ -361,9 +365,6 @@ __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(WHOLE)) rope_append
       prefetch_lines(a.v + u * a.v_stride + g0 * D, (g1 - g0) * D * 2, lane - 16);
     }
   }
-  const int n = a.n_tokens ? clamp_len(__ldg(a.n_tokens), a.n_cap) : a.n_cap;
-  const int pos = a.rot > 0 ? __ldg(a.positions + t) : 0;
-  if (t >= n) return;
   if (a.rot > 0 && (pos < 0 || pos >= a.table_rows)) return;  // no such angle: the token is left out
   if (query) {
     query_rows<D, INTER, WHOLE>(a, (int)t, pos, h0, h1);

@@ -59,6 +59,46 @@ def test_few_tokens_in_a_large_capacity(orc, n_tokens, kw):
     run(orc, N=1500, cap=1500, n_tokens=n_tokens, Hq=33, Hkv=3, G=32, seed=5 + n_tokens, **kw)
 
 
+def test_rows_behind_the_count_cost_nothing():
+    """16 tokens in a capacity of 16384 (32 / 8 heads of 128) take far less than the full capacity does: no row behind the
+    count travels.  A full call moves 369 MB, the q, k and v rows behind the count alone would be 201 MB."""
+    cap, Hq, Hkv = 16384, 32, 8
+    x = torch.randn(2, cap, Hq + 2 * Hkv, D, device="cuda").to(torch.bfloat16)
+    w = torch.ones(2, D, dtype=torch.bfloat16, device="cuda")
+    cache, out = pool(cap // 256, Hkv), torch.empty(cap, Hq, D, dtype=torch.bfloat16, device="cuda")
+    slots = torch.arange(cap, device="cuda")
+    table = torch.rand(cap, D // 2, 2, device="cuda")
+    pos = slots.to(torch.int32)
+
+    def micros(n):
+        """Device time of a call: twenty in a graph (an eager call's time is the host's), each on rows that the other
+        half's have pushed out of L2."""
+        count = torch.tensor([n], dtype=torch.int32, device="cuda")
+
+        def call(i):
+            y = x[i % 2]
+            append(count, slots, y[:, :Hq], y[:, Hq:Hq + Hkv], y[:, Hq + Hkv:], w[0], w[1], 1e-6, out, cache, pos=pos, table=table)
+
+        call(0)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            for i in range(20):
+                call(i)
+        times = []
+        for _ in range(5):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            g.replay()
+            b.record()
+            torch.cuda.synchronize()
+            times.append(a.elapsed_time(b) * 1e3 / 20)
+        return min(times)
+
+    few, full = micros(16), micros(cap)
+    assert few < 0.2 * full, f"16 tokens {few:.1f} us, {cap} tokens {full:.1f} us"
+
+
 def test_step_of_a_large_capacity_in_a_graph(orc):
     """Plan and append captured at a capacity of 16384 and replayed for steps of a few tokens: exact, and the rows behind
     the tokens stay as they were."""
