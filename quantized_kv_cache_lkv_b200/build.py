@@ -5,15 +5,18 @@ Each .cu file under csrc/ is compiled to an object under _build/ (in
 parallel), then all are linked into quantized_kv_cache_lkv_b200/liblkv.so
 with the CUDA runtime linked statically.  nvcc cross-compiles, so this works
 on a machine without a GPU.  csrc/binding.cpp is compiled by g++ against the
-headers of Python and torch.
+headers of Python and torch, after the library, which needs neither: where there
+is no torch, the library is all there is.
 """
 import concurrent.futures as cf
 import glob
+import importlib.metadata
 import os
 import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -63,11 +66,32 @@ def _compile(src, verbose):
     return obj, p.stderr
 
 
+def _native_key():
+    """What the module is built against, as the text that it carries; None without torch."""
+    try:
+        torch = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:
+        return None
+    return f"lkv _native for torch {torch}, {sysconfig.get_config_var('SOABI')}"
+
+
+def _native_is_current(key):
+    if not os.path.exists(NATIVE):
+        return False
+    newest = max(os.path.getmtime(f) for f in (os.path.join(CSRC, "binding.cpp"), os.path.join(ROOT, "include", "lkv.h"),
+                                               os.path.abspath(__file__)))
+    if os.path.getmtime(NATIVE) < newest:
+        return False
+    with open(NATIVE, "rb") as f:
+        return key.encode() + b"\0" in f.read()
+
+
 def build_native(force: bool = False) -> str:
     """_native.so: the torch libraries it needs are already loaded when it is imported."""
-    src = os.path.join(CSRC, "binding.cpp")
-    newest = max(os.path.getmtime(f) for f in (src, os.path.join(ROOT, "include", "lkv.h"), os.path.abspath(__file__)))
-    if not force and os.path.exists(NATIVE) and os.path.getmtime(NATIVE) >= newest:
+    key = _native_key()
+    if key is None:
+        raise ImportError("_native.so needs torch")
+    if not force and _native_is_current(key):
         return NATIVE
     import torch
     at = os.path.dirname(torch.__file__)
@@ -76,17 +100,17 @@ def build_native(force: bool = False) -> str:
            sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
     tmp = NATIVE + ".tmp"
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *("-I" + d for d in inc), src, "-o", tmp,
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f'-DLKV_NATIVE_KEY="{key}"',
+           *("-I" + d for d in inc), os.path.join(CSRC, "binding.cpp"), "-o", tmp,
            "-L" + os.path.join(at, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
     p = subprocess.run(cmd, capture_output=True, text=True)
     if p.returncode != 0:
-        raise RuntimeError(f"g++ failed for {src}:\n{p.stdout}\n{p.stderr}")
+        raise RuntimeError(f"g++ failed for binding.cpp:\n{p.stdout}\n{p.stderr}")
     os.replace(tmp, NATIVE)
     return NATIVE
 
 
-def build(force: bool = False, verbose: bool = False) -> str:
-    build_native(force)
+def build_library(force: bool = False, verbose: bool = False) -> str:
     srcs = _sources()
     newest = max(os.path.getmtime(f) for f in srcs + _headers() + [os.path.abspath(__file__)])
     if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= newest:
@@ -102,6 +126,16 @@ def build(force: bool = False, verbose: bool = False) -> str:
     subprocess.run([nvcc(), *ARCH, "-shared", "-o", tmp, *objs], check=True)
     os.replace(tmp, LIB)
     return LIB
+
+
+def build(force: bool = False, verbose: bool = False) -> str:
+    """liblkv.so, then _native.so where there is a torch to build it against."""
+    path = build_library(force, verbose)
+    try:
+        build_native(force)
+    except ImportError as e:
+        warnings.warn(f"{path} is built; {e}")
+    return path
 
 
 if __name__ == "__main__":

@@ -475,6 +475,10 @@ PyMethodDef g_methods[] = {
      "k_pool, k_sz_pool, v_pool, v_sz_pool, rule, out, lse, workspace, ws_bytes, stream=None)\n--\n\nThe call of include/lkv.h."},
     {nullptr, nullptr, 0, nullptr},
 };
+#ifdef LKV_NATIVE_KEY
+// What the module was built against: the build looks for it in the file.
+__attribute__((used)) const char g_key[] = LKV_NATIVE_KEY;
+#endif
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_native", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

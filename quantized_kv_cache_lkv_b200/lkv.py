@@ -8,6 +8,7 @@ in the CUDA kernels of liblkv.so, and there is no fallback -- if the library
 is missing, every call raises.
 """
 import ctypes
+import importlib
 import os
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -323,11 +324,13 @@ def native():
     global _nat
     if _nat is None:
         import torch  # noqa: F401  (its libraries come before the module's)
+        how = "build it with `python -m quantized_kv_cache_lkv_b200.build`"
         try:
-            from . import _native
-        except ImportError as e:
-            raise RuntimeError("the _native module is missing: build it with "
-                               "`python -m quantized_kv_cache_lkv_b200.build`") from e
+            _native = importlib.import_module("._native", __package__)
+        except ModuleNotFoundError as e:
+            raise RuntimeError(f"the _native module is missing: {how}") from e
+        except ImportError as e:  # built against another torch or Python
+            raise RuntimeError(f"the _native module does not load ({e}): {how} --force") from e
         L = lib()
         _native.connect(LkvError, *(ctypes.cast(getattr(L, n), ctypes.c_void_p).value for n in _NATIVE))
         globals().update({n: getattr(_native, n) for n in _NATIVE})
