@@ -534,12 +534,15 @@ typedef struct {
  *   lse = ln sum_t exp(x_t)
  * A query that sees nothing gets out = 0 and lse = -infinity; where a score
  * is not a number, neither are out and lse.  Arithmetic
- * keeps fp32 accuracy, and results do not depend on timing.  (scale, zero)
+ * keeps fp32 accuracy (of q, in channels above 2^-26 of the row's largest,
+ * unless K has 16 bits), and results do not depend on timing.  (scale, zero)
  * and 16-bit values at positions that no query of the sequence sees may be
  * anything, infinities and NaN among them.
  *
  *   max_q      most query rows of one sequence, 1 to 64: rows past it are not
- *              computed
+ *              computed.  It sets the launch: while max_q * Hq / Hkv <= 8, 8
+ *              query rows share a pass over a KV head's tokens, else 16, which
+ *              takes longer where fewer come
  *   n_rows     rows of q, out and lse
  *   seq_lens   in   int32 [B]
  *   cu_q       in   nullable int32 [B + 1], rising, within [0, n_rows]; rows

@@ -3,8 +3,9 @@ variants) and single-token decode attention over the packed cache, with the
 sparse-V skip and the attention-tiered cache.
 
 The compute lives in liblkv.so (hand-written sm_100a CUDA behind the C ABI of
-include/lkv.h); ``lkv`` is its thin ctypes binding, ``buffers`` allocates the
-device tensors, ``workloads`` draws seeded synthetic inputs.
+include/lkv.h); ``lkv`` is its binding (ctypes, and the native module _native for
+the calls of the serving step), ``buffers`` allocates the device tensors,
+``workloads`` draws seeded synthetic inputs.
 """
 from . import buffers, lkv, workloads  # noqa: F401
 

@@ -1124,9 +1124,7 @@ __device__ __forceinline__ void fetch_tile(const MultiArgs& a, Feed& f, uint8_t*
   }
 }
 
-// Joining the pieces p0 .. p1 - 1 of a cut unit (at(k) is where piece k lies):
-// first the weights 2^(ref_k - max) of a row, then the sums of the outputs,
-// whose loads do not depend on one another.  Pieces of other CTAs are read past L1.
+// Pieces of other CTAs are read past L1.
 template <bool L2, typename T>
 __device__ __forceinline__ T ld(const T* p) {
   if constexpr (L2) return __ldcg(p);

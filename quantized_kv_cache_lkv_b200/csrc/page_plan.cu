@@ -192,7 +192,7 @@ static cudaError_t launch_run(const PlanArgs& a, cudaStream_t s) {
 }
 
 cudaError_t launch_page_plan(const PlanArgs& a, cudaStream_t s) {
-  // a token per thread while one wave of blocks covers them
+  // a token per thread while one wave of blocks covers the capacity (how many there are, the host does not know)
   return a.n_cap <= num_sms() * kThreads ? launch_run<1>(a, s) : launch_run<4>(a, s);
 }
 

@@ -377,7 +377,8 @@ __global__ void __launch_bounds__(32 * kWarps, blocks_per_sm(WHOLE)) rope_append
 template <int D, bool INTER, bool WHOLE>
 cudaError_t launch_t(RopeAppendArgs a, cudaStream_t s) {
   constexpr int RPW = 32 / (D / kDimsPerLane);
-  // one batch of rows a warp while that leaves SMs idle, else runs of four and keys with values
+  // one batch of rows a warp while that leaves SMs idle, else runs of four and keys with values: by the capacity, as the
+  // host does not know the count
   const long long batches = (long long)a.n_cap * ((a.Hq + RPW - 1) / RPW);
   const bool many = batches >= (long long)num_sms() * 64;
   a.iters = many ? kRun : 1;

@@ -1,4 +1,5 @@
-"""Thin ctypes binding of liblkv (include/lkv.h).
+"""Binding of liblkv (include/lkv.h): ctypes, and for the calls of the serving step
+the native module _native, which checks the tensors.
 
 Functions carry the C names and argument order.  Tensor arguments may be
 torch tensors (their data_ptr() is passed) or raw integer addresses; the
