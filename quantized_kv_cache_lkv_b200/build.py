@@ -6,7 +6,8 @@ parallel), then all are linked into quantized_kv_cache_lkv_b200/liblkv.so
 with the CUDA runtime linked statically.  nvcc cross-compiles, so this works
 on a machine without a GPU.  csrc/binding.cpp is compiled by g++ against the
 headers of Python and torch, after the library, which needs neither: where there
-is no torch, the library is all there is.
+is no torch, the library is all there is (run this file itself then; the package
+imports torch).
 """
 import concurrent.futures as cf
 import glob
