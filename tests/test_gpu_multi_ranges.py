@@ -177,3 +177,18 @@ def test_scores_that_jump(orc, vb, jump):
     assert (np.abs(out.cpu().numpy() - want) <= REL * mag).all()
     # an lse of that size is off by 2^-24 of it for each of the eight sums of its score and for the logarithm's factor
     assert (np.abs(lse.cpu().numpy() - wl) <= 1e-5 * (1 + np.abs(wl))).all()
+
+
+@pytest.mark.parametrize("vb,G", [(4, 64), (8, 32)])
+@pytest.mark.parametrize("power", [-118, -112, -100, -60, 100])
+def test_v_near_the_ends_of_fp32(orc, vb, G, power):
+    """All of V tiny or huge, while scores of standard deviation 3 rise along the runs."""
+    D, T = 128, 600
+    k, v, q = make(24, 8, T, D, 2, 1, 13)
+    cache = cached(orc, 16, vb, G, k, v * 2.0 ** power, [T] * 24)
+    scale = float(np.float32(3.0 * D ** -0.5))
+    out, lse, _ = call(cache, q.cuda(), None, lkv.lkv_score_rule(3.0 * D ** -0.5), 1)
+    want, wl, mag = weights_and_values(q.float().numpy(), cache, [T] * 24, None, scale)
+    # scores of three times the size: three times the bound; and the steps of subnormal numbers
+    assert (np.abs(out.cpu().numpy() - want) <= 3 * REL * mag + 600 * 2.0 ** -149).all()
+    close_lse(lse.cpu().numpy(), wl)
