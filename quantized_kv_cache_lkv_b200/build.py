@@ -70,10 +70,14 @@ def _compile(src, verbose):
 def _native_key():
     """What the module is built against, as the text that it carries; None without torch."""
     try:
-        torch = importlib.metadata.version("torch")
-    except importlib.metadata.PackageNotFoundError:
-        return None
-    return f"lkv _native for torch {torch}, {sysconfig.get_config_var('SOABI')}"
+        version = importlib.metadata.version("torch")  # without importing it
+    except importlib.metadata.PackageNotFoundError:  # a source tree on the path, or none
+        try:
+            import torch
+        except ImportError:
+            return None
+        version = torch.__version__
+    return f"lkv _native for torch {version}, {sysconfig.get_config_var('SOABI')}"
 
 
 def _native_is_current(key):

@@ -68,6 +68,16 @@ def test_module_is_built_again_for_another_torch(monkeypatch):
     assert len(built) == 1 and any("torch 0.1" in word for word in built[0])
 
 
+def test_torch_without_a_distribution(monkeypatch):
+    """A source tree of torch on the path has no entry among the installed packages."""
+    def none(name):
+        raise importlib.metadata.PackageNotFoundError(name)
+
+    monkeypatch.setattr(importlib.metadata, "version", none)
+    import torch
+    assert f"torch {torch.__version__}," in build._native_key()
+
+
 @pytest.mark.parametrize("error,says", [(ImportError("undefined symbol: _ZN2at"), "does not load .*undefined symbol"),
                                         (ModuleNotFoundError("No module named '_native'"), "is missing")])
 def test_what_is_said_of_a_module_that_does_not_load(monkeypatch, error, says):
