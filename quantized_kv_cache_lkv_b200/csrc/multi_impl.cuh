@@ -48,7 +48,7 @@
 // in order, so results do not depend on timing.
 //
 // Measured on a B200, device time: K6V4, B16 x 8192, 32 / 8 heads, capped and
-// paged: 72 us for 201.7 MB (2.8 TB/s); 16 query rows over 131072 tokens: 124 us
+// paged: 73 us for 201.7 MB (2.8 TB/s); 16 query rows over 131072 tokens: 121 us
 // (113 before the units followed the products: 7% more instructions); 8-bit, G 32,
 // 64 ragged sequences behind a window of 1024: 59 us for 167 MB.
 #pragma once
@@ -700,7 +700,8 @@ __device__ __forceinline__ void v_product(const uint8_t* vc, const float* vsz, W
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             // the product first: beside a tiny scale the unit alone would take e out of fp32
-            const float x = e[nt][2 * j] * sz[2 * j][gi].x * w.u[nt][gi], y = e[nt][2 * j + 1] * sz[2 * j + 1][gi].x * w.u[nt][gi];
+            const float2 xy = exact_mul2(make_float2(e[nt][2 * j] * sz[2 * j][gi].x, e[nt][2 * j + 1] * sz[2 * j + 1][gi].x), f2(w.u[nt][gi]));
+            const float x = xy.x, y = xy.y;
             w.zacc[nt][gi] = fmaf(e[nt][2 * j], sz[2 * j][gi].y, fmaf(e[nt][2 * j + 1], sz[2 * j + 1][gi].y, w.zacc[nt][gi]));
             const uint32_t h = pack_f16(x, y);
             const float2 f = unpack_f16(h);
